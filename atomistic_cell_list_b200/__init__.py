@@ -24,7 +24,7 @@ E2F_OK = 0
 STATUS_NAMES = {0: "E2F_OK", 1: "E2F_ERR_INVALID_ARG", 2: "E2F_ERR_UNSUPPORTED", 3: "E2F_ERR_CAPACITY",
                 4: "E2F_ERR_ALIGNMENT", 5: "E2F_ERR_TIMEOUT", 6: "E2F_ERR_CUDA", 7: "E2F_ERR_NONFINITE",
                 8: "E2F_ERR_STALE"}
-E2F_F32, E2F_BF16 = 0, 1
+E2F_F32, E2F_BF16, E2F_MXI8 = 0, 1, 2
 
 
 class E2FError(RuntimeError):
@@ -41,6 +41,16 @@ class e2f_attn_cfg(ctypes.Structure):
 class e2f_sixj_cfg(ctypes.Structure):
     _fields_ = [("L", ctypes.c_int), ("Lf", ctypes.c_int), ("C", ctypes.c_int), ("H", ctypes.c_int),
                 ("n_rbf", ctypes.c_int), ("cutoff", ctypes.c_float)]
+
+
+class e2f_norm_cfg(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("C", ctypes.c_int), ("eps", ctypes.c_float), ("x_dtype", ctypes.c_int),
+                ("y_dtype", ctypes.c_int)]
+
+
+class e2f_embed_cfg(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int), ("C", ctypes.c_int), ("n_tokens", ctypes.c_int), ("scale", ctypes.c_float),
+                ("table_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
 _lib = None
@@ -80,6 +90,14 @@ _SIGS = {
     "e2f_sixj_workspace_size": (_sz, [_i64, ctypes.POINTER(e2f_sixj_cfg)]),
     "e2f_sixj_attention": (ctypes.c_int, [ctypes.POINTER(e2f_sixj_cfg), _vp, _i64, _vp, ctypes.c_int32, _vp, _vp,
                                           _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "e2f_layer_norm": (ctypes.c_int, [ctypes.POINTER(e2f_norm_cfg), _i64] + [_vp] * 12),
+    "e2f_layer_norm_backward_workspace_size": (_sz, [_i64, ctypes.POINTER(e2f_norm_cfg)]),
+    "e2f_layer_norm_backward": (ctypes.c_int, [ctypes.POINTER(e2f_norm_cfg), _i64] + [_vp] * 11 + [_sz, _vp]),
+    "e2f_checkpoint_store": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int, _vp, _vp, _vp]),
+    "e2f_checkpoint_load": (ctypes.c_int, [_vp, _vp, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp]),
+    "e2f_embedding": (ctypes.c_int, [ctypes.POINTER(e2f_embed_cfg), _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
+    "e2f_embedding_backward_workspace_size": (_sz, [_i64, ctypes.POINTER(e2f_embed_cfg)]),
+    "e2f_embedding_backward": (ctypes.c_int, [ctypes.POINTER(e2f_embed_cfg), _vp, _i64, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -423,6 +441,202 @@ def e2f_sixj_attention(cfg: e2f_sixj_cfg, pos, row_ptr, col, x, W_q, W_k, W_rad,
                                     _ptr(w_path), _ptr(out), _ptr(workspace), workspace.numel(), _stream(stream))
     _check(code, "e2f_sixj_attention")
     return out
+
+
+_DTYPES = {"f32": E2F_F32, "bf16": E2F_BF16, "mxi8": E2F_MXI8}
+_TORCH = {E2F_F32: torch.float32, E2F_BF16: torch.bfloat16, E2F_MXI8: torch.int8}
+
+
+def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device=None) -> int:
+    """Address of a tensor that must be contiguous, of this dtype and shape, and on the current CUDA device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    if device is None:
+        if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name} must be on the current CUDA device")
+    elif t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """New memory for a call on `stream` (None: the current one), from that stream's pool."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _on(stream) -> int:
+    """Handle of the stream of a call (None: the current one); it must belong to the current device."""
+    if stream is not None and stream.device_index != torch.cuda.current_device():
+        raise ValueError("stream must belong to the current CUDA device")
+    return _stream(stream)
+
+
+def _result(out: dict, name: str, dtype: torch.dtype, shape, device, stream) -> int:
+    """Address of out[name], allocated here when the caller did not give it."""
+    t = out.get(name)
+    if t is None:
+        t = out[name] = _empty(shape, dtype, device, stream)
+        return t.data_ptr()
+    return _operand(f"out[{name!r}]", t, dtype, shape, device)
+
+
+def _scratch(workspace, n_bytes: int, device, stream) -> torch.Tensor:
+    """The caller's workspace, or a new one when it is absent or too small."""
+    if workspace is None or workspace.numel() < n_bytes:
+        return _empty(max(n_bytes, 256), torch.uint8, device, stream)
+    if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def make_norm_cfg(L: int, C: int, x_dtype: str = "f32", y_dtype: str = "bf16", eps: float = 1e-5) -> e2f_norm_cfg:
+    """x_dtype: "f32", "bf16" or "mxi8" (x is an 8-bit checkpoint); y_dtype: "f32" or "bf16"."""
+    return e2f_norm_cfg(int(L), int(C), float(eps), _DTYPES[x_dtype], _DTYPES[y_dtype])
+
+
+def e2f_layer_norm(cfg: e2f_norm_cfg, x, weight, bias=None, residual=None, x_scales=None, checkpoint: bool = False,
+                   stats: bool = True, out: dict | None = None, stream=None) -> dict:
+    """Layer norm of x[N, (L+1)^2, C] (see include/e2f.h): a dict with y, with stats mean and rstd, with
+    residual sum, and with checkpoint codes and scales of what was normalised. Tensors given in `out`
+    under these names are written in place of new ones; out["sum"] may be x."""
+    L, C = cfg.L, cfg.C
+    K, n = (L + 1) ** 2, x.shape[0] if x.dim() else 0
+    shape, dev = torch.Size((n, K, C)), x.device
+    xt = _TORCH[cfg.x_dtype]
+    px = _operand("x", x, xt, shape)
+    pw = _operand("weight", weight, torch.float32, (L + 1, C), dev)
+    pb = None if bias is None else _operand("bias", bias, torch.float32, (C,), dev)
+    pr = ps = psum = pm = pi = pc = pcs = None
+    nb = (C + 31) // 32
+    res = {} if out is None else dict(out)
+    if cfg.x_dtype == E2F_MXI8:
+        if x_scales is None:
+            raise ValueError("an mxi8 input needs x_scales")
+        ps = _operand("x_scales", x_scales, torch.uint8, (n, K, nb), dev)
+    if residual is not None:
+        pr = _operand("residual", residual, torch.float32, shape, dev)
+        psum = _result(res, "sum", xt, shape, dev, stream)
+    py = _result(res, "y", _TORCH[cfg.y_dtype], shape, dev, stream)
+    if stats:
+        pm = _result(res, "mean", torch.float32, (n,), dev, stream)
+        pi = _result(res, "rstd", torch.float32, (n, L + 1), dev, stream)
+    if checkpoint:
+        pc = _result(res, "codes", torch.int8, shape, dev, stream)
+        pcs = _result(res, "scales", torch.uint8, (n, K, nb), dev, stream)
+    _check(lib().e2f_layer_norm(ctypes.byref(cfg), n, px, ps, pr, pw, pb, psum, py, pm, pi, pc, pcs, _on(stream)),
+           "e2f_layer_norm")
+    return res
+
+
+def e2f_layer_norm_backward_workspace_size(n_atoms: int, cfg: e2f_norm_cfg) -> int:
+    return int(lib().e2f_layer_norm_backward_workspace_size(int(n_atoms), ctypes.byref(cfg)))
+
+
+def e2f_layer_norm_backward(cfg: e2f_norm_cfg, x, weight, mean, rstd, grad_y, grad_skip=None, x_scales=None,
+                            want_weights: bool = True, workspace: torch.Tensor | None = None,
+                            out: dict | None = None, stream=None) -> dict:
+    """Gradients of e2f_layer_norm (see include/e2f.h): a dict with x and, when want_weights, weight and bias
+    (all fp32). out["x"] may be grad_skip or grad_y."""
+    L, C = cfg.L, cfg.C
+    K, n = (L + 1) ** 2, x.shape[0] if x.dim() else 0
+    shape, dev, f32 = torch.Size((n, K, C)), x.device, torch.float32
+    px = _operand("x", x, _TORCH[cfg.x_dtype], shape)
+    ps = None
+    if cfg.x_dtype == E2F_MXI8:
+        if x_scales is None:
+            raise ValueError("an mxi8 input needs x_scales")
+        ps = _operand("x_scales", x_scales, torch.uint8, (n, K, (C + 31) // 32), dev)
+    pw = _operand("weight", weight, f32, (L + 1, C), dev)
+    pm = _operand("mean", mean, f32, (n,), dev)
+    pi = _operand("rstd", rstd, f32, (n, L + 1), dev)
+    pg = _operand("grad_y", grad_y, f32, shape, dev)
+    pk = None if grad_skip is None else _operand("grad_skip", grad_skip, f32, shape, dev)
+    g = {} if out is None else dict(out)
+    pgx = _result(g, "x", f32, shape, dev, stream)
+    pgw = pgb = None
+    if want_weights:
+        pgw = _result(g, "weight", f32, (L + 1, C), dev, stream)
+        pgb = _result(g, "bias", f32, (C,), dev, stream)
+    workspace = _scratch(workspace, e2f_layer_norm_backward_workspace_size(n, cfg), dev, stream)
+    _check(lib().e2f_layer_norm_backward(ctypes.byref(cfg), n, px, ps, pw, pm, pi, pg, pk, pgx, pgw, pgb,
+                                         workspace.data_ptr(), workspace.numel(), _on(stream)),
+           "e2f_layer_norm_backward")
+    return g
+
+
+def e2f_checkpoint_store(x: torch.Tensor, out: dict | None = None, stream=None):
+    """(codes int8 [..., C], scales uint8 [..., ceil(C/32)]): the 8-bit checkpoint of x[..., C], fp32 or bf16
+    (see include/e2f.h). Tensors given in `out` as codes and scales are written in place of new ones."""
+    if x.dim() < 1 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be an fp32 or bf16 tensor of at least one dimension")
+    px, C = _operand("x", x, x.dtype, x.shape), x.shape[-1]
+    res = {} if out is None else dict(out)
+    pc = _result(res, "codes", torch.int8, x.shape, x.device, stream)
+    ps = _result(res, "scales", torch.uint8, x.shape[:-1] + ((C + 31) // 32,), x.device, stream)
+    _check(lib().e2f_checkpoint_store(px, E2F_F32 if x.dtype is torch.float32 else E2F_BF16,
+                                      x.numel() // max(C, 1), C, pc, ps, _on(stream)), "e2f_checkpoint_store")
+    return res["codes"], res["scales"]
+
+
+def e2f_checkpoint_load(codes: torch.Tensor, scales: torch.Tensor, dtype: str = "f32",
+                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The values (fp32 or bf16) that a checkpoint stands for (see include/e2f.h)."""
+    if codes.dim() < 1 or dtype not in ("f32", "bf16"):
+        raise ValueError("codes must have at least one dimension and dtype be f32 or bf16")
+    pc, C = _operand("codes", codes, torch.int8, codes.shape), codes.shape[-1]
+    ps = _operand("scales", scales, torch.uint8, codes.shape[:-1] + ((C + 31) // 32,), codes.device)
+    res = {} if out is None else {"out": out}
+    po = _result(res, "out", _TORCH[_DTYPES[dtype]], codes.shape, codes.device, stream)
+    _check(lib().e2f_checkpoint_load(pc, ps, codes.numel() // max(C, 1), C, _DTYPES[dtype], po, _on(stream)),
+           "e2f_checkpoint_load")
+    return res["out"]
+
+
+def make_embed_cfg(n_tokens: int, C: int, L: int = 0, scale: float = 1.0, table_dtype: str = "f32",
+                   out_dtype: str = "f32") -> e2f_embed_cfg:
+    return e2f_embed_cfg(int(L), int(C), int(n_tokens), float(scale), _DTYPES[table_dtype], _DTYPES[out_dtype])
+
+
+def e2f_embedding(cfg: e2f_embed_cfg, tokens, table, out: torch.Tensor | None = None, stream=None,
+                  check: bool = True) -> torch.Tensor:
+    """out[N, (L+1)^2, C]: scaled table rows of int32 tokens as degree-0 features (see include/e2f.h). Negative
+    tokens are padding. With check, a token beyond the table raises E2FError (this waits for the stream)."""
+    n, dev = tokens.shape[0] if tokens.dim() else 0, tokens.device
+    pt = _operand("tokens", tokens, torch.int32, (n,))
+    pw = _operand("table", table, _TORCH[cfg.table_dtype], (cfg.n_tokens, cfg.C), dev)
+    res = {} if out is None else {"out": out}
+    po = _result(res, "out", _TORCH[cfg.out_dtype], (n, (cfg.L + 1) ** 2, cfg.C), dev, stream)
+    ws = _empty(256, torch.uint8, dev, stream) if check else None
+    s = _on(stream)
+    _check(lib().e2f_embedding(ctypes.byref(cfg), pt, n, pw, po, _ptr(ws), 256 if check else 0, s), "e2f_embedding")
+    if check:
+        _check(lib().e2f_attention_status(_ptr(ws), 256, s), "e2f_embedding (device)")
+    return res["out"]
+
+
+def e2f_embedding_backward_workspace_size(n_atoms: int, cfg: e2f_embed_cfg) -> int:
+    return int(lib().e2f_embedding_backward_workspace_size(int(n_atoms), ctypes.byref(cfg)))
+
+
+def e2f_embedding_backward(cfg: e2f_embed_cfg, tokens, grad_out, workspace: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None, stream=None, check: bool = True) -> torch.Tensor:
+    """grad_table[n_tokens, C] fp32 of e2f_embedding from grad_out[N, (L+1)^2, C] fp32 (see include/e2f.h)."""
+    n, dev = tokens.shape[0] if tokens.dim() else 0, tokens.device
+    pt = _operand("tokens", tokens, torch.int32, (n,))
+    pg = _operand("grad_out", grad_out, torch.float32, (n, (cfg.L + 1) ** 2, cfg.C), dev)
+    res = {} if out is None else {"out": out}
+    po = _result(res, "out", torch.float32, (cfg.n_tokens, cfg.C), dev, stream)
+    workspace = _scratch(workspace, e2f_embedding_backward_workspace_size(n, cfg), dev, stream)
+    s = _on(stream)
+    _check(lib().e2f_embedding_backward(ctypes.byref(cfg), pt, n, pg, po, _ptr(workspace), workspace.numel(), s),
+           "e2f_embedding_backward")
+    if check:
+        _check(lib().e2f_attention_status(_ptr(workspace), workspace.numel(), s), "e2f_embedding_backward (device)")
+    return res["out"]
 
 
 # short aliases

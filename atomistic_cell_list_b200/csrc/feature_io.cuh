@@ -1,0 +1,138 @@
+// Vector loads and stores of node features (fp32, bf16 or 8-bit checkpoint)
+// and the checkpoint's block format, shared by the norm, embedding and
+// checkpoint kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace e2f {
+
+constexpr int kCkBlock = 32;  // channels that share one scale byte
+__host__ __device__ inline int ck_blocks(int C) { return (C + kCkBlock - 1) / kCkBlock; }
+
+enum { kF32 = 0, kBF16 = 1, kMXI8 = 2 };  // e2f_dtype values, as template arguments
+
+// V consecutive values of an fp32 or bf16 array (V = 4: address 4-value aligned)
+template <int T, int V>
+__device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&v)[V]) {
+    if constexpr (T == kF32) {
+        const float* q = static_cast<const float*>(p) + i;
+        if constexpr (V == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(q);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        } else {
+            for (int k = 0; k < V; ++k) v[k] = q[k];
+        }
+    } else {
+        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p) + i;
+        if constexpr (V == 4) {
+            const uint2 a = *reinterpret_cast<const uint2*>(q);
+            v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+            v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+        } else {
+            for (int k = 0; k < V; ++k) v[k] = __bfloat162float(q[k]);
+        }
+    }
+}
+
+template <int T, int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[V]) {
+    if constexpr (T == kF32) {
+        float* q = static_cast<float*>(p) + i;
+        if constexpr (V == 4) {
+            *reinterpret_cast<float4*>(q) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            for (int k = 0; k < V; ++k) q[k] = v[k];
+        }
+    } else {
+        __nv_bfloat16* q = static_cast<__nv_bfloat16*>(p) + i;
+        if constexpr (V == 4) {
+            __nv_bfloat162 a[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+            *reinterpret_cast<uint2*>(q) = *reinterpret_cast<uint2*>(a);
+        } else {
+            for (int k = 0; k < V; ++k) q[k] = __float2bfloat16_rn(v[k]);
+        }
+    }
+}
+
+// fp32 value as storage type T keeps it
+template <int T>
+__device__ __forceinline__ float as_stored(float v) {
+    if constexpr (T == kBF16) return __bfloat162float(__float2bfloat16_rn(v));
+    return v;
+}
+
+// 2^(s - 127) for a scale byte; 255 marks a block that held a NaN or an infinity
+__device__ __forceinline__ float ck_scale(uint32_t s) {
+    return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+}
+
+// scale byte of a block from the largest magnitude bits in it: the exponent of
+// the largest value, at least 2^-120 so that the unit 2^(e-6) and its inverse
+// are normal numbers
+__device__ __forceinline__ uint32_t ck_byte(uint32_t max_bits) { return max(max_bits >> 23, 7u); }
+
+__device__ __forceinline__ uint32_t ck_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// code of v in a block of scale byte s: rint(v 2^(6-e)) clamped to +-127. The
+// scaling is a power of two, so the code does not depend on how it is computed.
+__device__ __forceinline__ int ck_code(float v, uint32_t s) {
+    if (s == 255u) return 0;
+    return min(127, max(-127, __float2int_rn(v * __uint_as_float((260u - s) << 23))));
+}
+
+// V decoded channels c .. c+V-1 of row `row` of a checkpoint (V = 4: c a multiple of 4, codes 4-byte aligned)
+template <int V>
+__device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* scales, int64_t row, int C, int nb,
+                                           int c, float (&v)[V]) {
+    const float u = ck_scale(scales[row * nb + c / kCkBlock]);
+    const int8_t* q = codes + row * C + c;
+    if constexpr (V == 4) {
+        const char4 a = *reinterpret_cast<const char4*>(q);
+        v[0] = a.x * 0.015625f * u; v[1] = a.y * 0.015625f * u;
+        v[2] = a.z * 0.015625f * u; v[3] = a.w * 0.015625f * u;
+    } else {
+        for (int k = 0; k < V; ++k) v[k] = q[k] * 0.015625f * u;
+    }
+}
+
+// features of any storage: fp32, bf16, or a checkpoint (codes at p, scales at s)
+template <int T, int V>
+__device__ __forceinline__ void load_feat(const void* p, const uint8_t* s, int64_t row, int C, int nb, int c,
+                                          float (&v)[V]) {
+    if constexpr (T == kMXI8) {
+        load_codes<V>(static_cast<const int8_t*>(p), s, row, C, nb, c, v);
+    } else {
+        load_vec<T, V>(p, row * C + c, v);
+    }
+}
+
+// Checkpoint of V channels per lane, lanes in channel order: a block of 32
+// channels is 32/V lanes (of one team of `team` lanes, when rows are shorter).
+// Every lane of the warp calls it; lanes beyond the row pass ok = false.
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int64_t row, int C, int nb, int c, bool ok,
+                                            int team, const float (&v)[V]) {
+    uint32_t m = 0;
+    if (ok)
+        for (int k = 0; k < V; ++k) m = max(m, ck_mag(v[k]));
+    constexpr int G = kCkBlock / V;
+    for (int o = 1; o < G; o <<= 1)
+        if (o < team) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (!ok) return;
+    const uint32_t s = ck_byte(m);
+    int8_t* q = codes + row * C + c;
+    if constexpr (V == 4) {
+        char4 a;
+        a.x = (signed char)ck_code(v[0], s); a.y = (signed char)ck_code(v[1], s);
+        a.z = (signed char)ck_code(v[2], s); a.w = (signed char)ck_code(v[3], s);
+        *reinterpret_cast<char4*>(q) = a;
+    } else {
+        for (int k = 0; k < V; ++k) q[k] = (int8_t)ck_code(v[k], s);
+    }
+    if (c % kCkBlock == 0) scales[row * nb + c / kCkBlock] = (uint8_t)s;
+}
+
+}  // namespace e2f

@@ -43,7 +43,9 @@ typedef enum {
     E2F_ERR_STALE = 8         /* reused cell lists: an atom moved > skin/2   */
 } e2f_status;
 
-typedef enum { E2F_F32 = 0, E2F_BF16 = 1 } e2f_dtype;
+/* E2F_MXI8: an 8-bit checkpoint (codes with a scale byte per 32 channels), an
+ * input type of e2f_layer_norm and e2f_layer_norm_backward only. */
+typedef enum { E2F_F32 = 0, E2F_BF16 = 1, E2F_MXI8 = 2 } e2f_dtype;
 
 /* Layer shape. L = highest degree (0..4); C = channels (multiple of 16,
  * 16..256); H = attention heads (divides C); n_rbf = radial basis size
@@ -511,6 +513,168 @@ e2f_status e2f_sixj_attention(const e2f_sixj_cfg* cfg, const float* pos, int64_t
                               const float* W_k, const float* W_rad,
                               const float* w_path, float* out, void* workspace,
                               size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Layer norm of irreducible features: what stands between two attention
+ * layers. The pages name no norm; this is the plain equivariant one, and at
+ * L = 0 the ordinary layer norm of rows of C values. For each node and
+ * degree l, over the group of 2l+1 rows of C channels of
+ *   h = x, or h = round(x + residual): the fp32 sum rounded to x_dtype,
+ *       which is also written to `sum` (the residual stream),
+ *   mu   = mean_c h[0,c];   d = h - mu for l = 0, d = h for l >= 1
+ *   rstd = 1/sqrt(mean_{m,c} d^2 + eps)
+ *   y[lm,c] = weight[l,c] d rstd  (+ bias[c] for l = 0)
+ * A degree's rows share one factor and the mean touches l = 0 only, so the
+ * norm commutes with rotations. A NaN or an infinity reaches the outputs of
+ * its own group and nothing else. Sums are fp32; groups whose d^2 leaves the
+ * fp32 range (|d| above about 1e19) give rstd = 0.
+ *
+ *   cfg        host; L (0..4), C (1..16384), eps > 0, x_dtype (E2F_F32,
+ *              E2F_BF16 or E2F_MXI8: x is a checkpoint), y_dtype (E2F_F32 or
+ *              E2F_BF16).
+ *   x          device, [N, (L+1)^2, C] of x_dtype (codes for E2F_MXI8).
+ *   x_scales   device, uint8 [N, (L+1)^2, ceil(C/32)] for E2F_MXI8, else
+ *              ignored.
+ *   residual   device, float [N, (L+1)^2, C] (the attention's output), or
+ *              NULL. E2F_ERR_UNSUPPORTED with E2F_MXI8.
+ *   weight     device, float [L+1, C];  bias  device, float [C] or NULL.
+ *   sum        device, x_dtype, written; given exactly when residual is. May
+ *              be x itself (the residual stream is then updated in place).
+ *   y          device, y_dtype, written; overlaps no input.
+ *   mean, rstd device, float [N] and [N, L+1], written; either may be NULL.
+ *   ck_codes, ck_scales  device, written with the 8-bit checkpoint of h
+ *              (e2f_checkpoint_store); both or neither. E2F_ERR_UNSUPPORTED
+ *              with E2F_MXI8.
+ * 16-byte alignment for every pointer but x_scales, ck_scales, mean and
+ * rstd (E2F_ERR_ALIGNMENT). No workspace. Asynchronous, may be captured into
+ * a graph.
+ *
+ * A layer keeps only its checkpoint between forward and backward. In the
+ * backward pass e2f_layer_norm on the checkpoint (x_dtype E2F_MXI8) gives
+ * the features again for e2f_onfly_attention_backward, with the statistics
+ * that e2f_layer_norm_backward takes together with the checkpoint.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int L;
+    int C;
+    float eps;
+    e2f_dtype x_dtype;
+    e2f_dtype y_dtype;
+} e2f_norm_cfg;
+
+e2f_status e2f_layer_norm(const e2f_norm_cfg* cfg, int64_t n_atoms, const void* x,
+                          const uint8_t* x_scales, const float* residual,
+                          const float* weight, const float* bias, void* sum,
+                          void* y, float* mean, float* rstd, int8_t* ck_codes,
+                          uint8_t* ck_scales, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gradients of e2f_layer_norm, given grad_y = dLoss/dy. With
+ * xh = d rstd and u = grad_y weight, means over the (node, degree) group:
+ *   grad_x = rstd (u - xh mean(u xh))             l >= 1
+ *   grad_x = rstd (u - mean(u) - xh mean(u xh))   l = 0
+ *   grad_x += grad_skip                           when given
+ *   grad_weight[l,c] = sum_{n,m} grad_y xh;  grad_bias[c] = sum_n grad_y[n,0,c]
+ *
+ *   cfg        y_dtype is ignored.
+ *   x, x_scales  the h that was normalised: x, or `sum`, or its checkpoint.
+ *   weight, mean, rstd  as in the forward (the statistics of this x).
+ *   grad_y     device, float [N, (L+1)^2, C].
+ *   grad_skip  device, float, same shape, or NULL: the gradient that reaches
+ *              h past the norm (the residual stream's); grad_x is then the
+ *              gradient of both x and residual.
+ *   grad_x     device, float, written; may be grad_skip or grad_y itself.
+ *   grad_weight, grad_bias  device, float [L+1, C] and [C], written; either
+ *              may be NULL (not computed).
+ *   workspace  device, >= e2f_layer_norm_backward_workspace_size(...) bytes,
+ *              256-byte aligned, not shared by calls in flight (a captured
+ *              call keeps using it at every replay).
+ * 16-byte alignment for every pointer but x_scales, mean and rstd. All sums
+ * have a fixed order: results repeat bit for bit. N = 0 writes zero weight
+ * gradients. Asynchronous, may be captured into a graph.
+ * ---------------------------------------------------------------------- */
+size_t e2f_layer_norm_backward_workspace_size(int64_t n_atoms, const e2f_norm_cfg* cfg);
+
+e2f_status e2f_layer_norm_backward(const e2f_norm_cfg* cfg, int64_t n_atoms,
+                                   const void* x, const uint8_t* x_scales,
+                                   const float* weight, const float* mean,
+                                   const float* rstd, const float* grad_y,
+                                   const float* grad_skip, float* grad_x,
+                                   float* grad_weight, float* grad_bias,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit activation checkpoints. Blocks of 32 channels of one row (the last
+ * one of a row may be shorter) share a power of two:
+ *   e = max(-120, floor(log2 max|x|)) of the block
+ *   code = rint(x 2^(6-e)) clamped to +-127 (round half to even)
+ *   scale byte = e + 127;  the block stands for code 2^(e-6)
+ * the 8-bit integer microscaling format (element unit 2^-6, power-of-two
+ * scale byte) of the OCP Microscaling Formats specification. A block that
+ * holds a NaN or an infinity gets scale byte 255 and stands for NaN
+ * throughout. Every scaling is exact, so codes do not depend on the
+ * evaluation, decoded values are exact in fp32 and in bf16 (e >= -120), and
+ * a value is off by at most max(2^(e-7), one unit 2^(e-6) at the clamp).
+ * (C + ceil(C/32)) bytes a row instead of 4C or 2C.
+ *
+ *   x, out     device, [rows, C] of dtype (E2F_F32 or E2F_BF16), 16-byte
+ *              aligned.
+ *   rows, C    rows >= 0, C >= 1.
+ *   codes      device, int8 [rows, C], 16-byte aligned.
+ *   scales     device, uint8 [rows, ceil(C/32)].
+ * Buffers of one call do not overlap. Asynchronous, may be captured.
+ * ---------------------------------------------------------------------- */
+e2f_status e2f_checkpoint_store(const void* x, e2f_dtype dtype, int64_t rows, int C,
+                                int8_t* codes, uint8_t* scales, void* stream);
+
+e2f_status e2f_checkpoint_load(const int8_t* codes, const uint8_t* scales,
+                               int64_t rows, int C, e2f_dtype dtype, void* out,
+                               void* stream);
+
+/* ------------------------------------------------------------------------
+ * Species embedding: the features that enter the first layer, and their
+ * gradient with respect to the table (the pages start from given features).
+ *   out[n,0,c] = scale table[token_n, c],  out[n,k,c] = 0 for k >= 1
+ *   grad_table[v,c] = scale sum_{n: token_n = v} grad_out[n,0,c]
+ * A negative token marks a padding atom: zero features, no gradient. A token
+ * >= n_tokens is treated the same and recorded as E2F_ERR_INVALID_ARG in the
+ * status word at the start of the workspace (read it with
+ * e2f_attention_status).
+ *
+ *   cfg        host; L (0..4), C (1..16384), n_tokens >= 1 rows of the
+ *              table, scale, table_dtype and out_dtype (E2F_F32, E2F_BF16).
+ *   tokens     device, int32 [N].
+ *   table      device, [n_tokens, C] of table_dtype.
+ *   out        device, [N, (L+1)^2, C] of out_dtype, written.
+ *   grad_out   device, float [N, (L+1)^2, C]; the rows k >= 1 are not read.
+ *   grad_table device, float [n_tokens, C], written (rows of tokens that do
+ *              not occur become zero).
+ *   workspace  forward: NULL (tokens >= n_tokens go unreported) or >= 256
+ *              bytes; backward: >= e2f_embedding_backward_workspace_size
+ *              bytes. 256-byte aligned, not shared by calls in flight.
+ * table, out, grad_out, grad_table 16-byte aligned. The backward sorts the
+ * tokens and sums each token's rows in a fixed order: results repeat bit for
+ * bit. Asynchronous, may be captured into a graph.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+    int L;
+    int C;
+    int n_tokens;
+    float scale;
+    e2f_dtype table_dtype;
+    e2f_dtype out_dtype;
+} e2f_embed_cfg;
+
+e2f_status e2f_embedding(const e2f_embed_cfg* cfg, const int32_t* tokens, int64_t n_atoms,
+                         const void* table, void* out, void* workspace,
+                         size_t ws_bytes, void* stream);
+
+size_t e2f_embedding_backward_workspace_size(int64_t n_atoms, const e2f_embed_cfg* cfg);
+
+e2f_status e2f_embedding_backward(const e2f_embed_cfg* cfg, const int32_t* tokens,
+                                  int64_t n_atoms, const float* grad_out,
+                                  float* grad_table, void* workspace,
+                                  size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
