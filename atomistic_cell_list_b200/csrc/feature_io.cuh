@@ -83,18 +83,63 @@ __device__ __forceinline__ int ck_code(float v, uint32_t s) {
     return min(127, max(-127, __float2int_rn(v * __uint_as_float((260u - s) << 23))));
 }
 
+// A code byte as fp32, without a conversion instruction: the byte with its sign
+// bit turned over is code + 128, placed in the low mantissa of 2^23.
+__device__ __forceinline__ float ck_value(uint32_t biased_byte) {
+    return __uint_as_float(0x4b000000u | biased_byte) - 8388736.f;
+}
+
+// Four channels as storage keeps them, so that loads can be issued in a batch
+// before any value is used.
+template <int T>
+struct Raw4;
+template <>
+struct Raw4<kF32> {
+    float4 a;
+    __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
+        a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    }
+};
+template <>
+struct Raw4<kBF16> {
+    uint2 a;
+    __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
+        a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+        v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+    }
+};
+template <>
+struct Raw4<kMXI8> {
+    uint32_t a, s;
+    __device__ __forceinline__ void load(const void* p, const uint8_t* scales, int64_t i, int64_t block) {
+        a = *reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(p) + i);
+        s = scales[block];
+    }
+    __device__ __forceinline__ void get(float (&v)[4]) const {
+        const float u = ck_scale(s) * 0.015625f;  // exact: at least 2^-133
+        const uint32_t b = a ^ 0x80808080u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = ck_value((b >> (8 * k)) & 255u) * u;
+    }
+};
+
 // V decoded channels c .. c+V-1 of row `row` of a checkpoint (V = 4: c a multiple of 4, codes 4-byte aligned)
 template <int V>
 __device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* scales, int64_t row, int C, int nb,
                                            int c, float (&v)[V]) {
-    const float u = ck_scale(scales[row * nb + c / kCkBlock]);
-    const int8_t* q = codes + row * C + c;
     if constexpr (V == 4) {
-        const char4 a = *reinterpret_cast<const char4*>(q);
-        v[0] = a.x * 0.015625f * u; v[1] = a.y * 0.015625f * u;
-        v[2] = a.z * 0.015625f * u; v[3] = a.w * 0.015625f * u;
+        Raw4<kMXI8> r;
+        r.load(codes, scales, row * C + c, row * nb + c / kCkBlock);
+        r.get(v);
     } else {
-        for (int k = 0; k < V; ++k) v[k] = q[k] * 0.015625f * u;
+        const float u = ck_scale(scales[row * nb + c / kCkBlock]) * 0.015625f;
+        for (int k = 0; k < V; ++k) v[k] = codes[row * C + c + k] * u;
     }
 }
 

@@ -9,49 +9,61 @@ __device__ __forceinline__ void norm_unit(const NormArgs& a, int64_t node0, int6
     constexpr int R = 2 * l + 1, B = nodes_of(l, fwd_rows(NI)), V = 4;
     const int lane = threadIdx.x & 31, t = lane & (TL - 1), teams = 32 / TL, K = (a.L + 1) * (a.L + 1);
     const int64_t first = node0 + lane / TL;  // a warp's teams take every `teams`-th node
-    const int64_t row0 = first * K + l * l, base = row0 * a.C + t * V;
-    const int step = teams * K;               // rows between two nodes of a team
     const int have = (int)min((int64_t)B * teams, end - first);  // node b exists: b teams < have
+    // loads are not predicated: a missing node reads the chunk's last one, a lane beyond the row its first
+    // channels, so that all of a unit's loads are in flight at once
     bool in[NI];
-    float v[B][R][NI][V];
+    int row[B], off[B][NI];
+    const int64_t row0 = min(first, end - 1) * K + l * l, base = row0 * a.C;
 #pragma unroll
     for (int i = 0; i < NI; ++i) in[i] = (t + TL * i) * V < a.C;
 #pragma unroll
-    for (int b = 0; b < B; ++b)
+    for (int b = 0; b < B; ++b) {
+        row[b] = b * teams < have ? b * teams * K : 0;
 #pragma unroll
-        for (int m = 0; m < R; ++m)
+        for (int i = 0; i < NI; ++i) off[b][i] = row[b] * a.C + (in[i] ? (t + TL * i) * V : 0);
+    }
+    float v[B][R][NI][V];
+    {
+        Raw4<XT> raw[B][R][NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                for (int k = 0; k < V; ++k) v[b][m][i][k] = 0.f;
-                if (b * teams < have && in[i]) {
-                    if constexpr (XT == kMXI8)
-                        load_codes<V>(static_cast<const int8_t*>(a.x), a.xs, row0 + b * step + m, a.C, a.nb,
-                                      (t + TL * i) * V, v[b][m][i]);
-                    else
-                        load_vec<XT, V>(a.x, base + ((b * step + m) * a.C + TL * i * V), v[b][m][i]);
-                }
-            }
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    raw[b][m][i].load(a.x, a.xs, base + (off[b][i] + m * a.C),
+                                      (row0 + row[b] + m) * a.nb + (in[i] ? (t + TL * i) * V / kCkBlock : 0));
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) raw[b][m][i].get(v[b][m][i]);
+    }
     if constexpr (XT != kMXI8) {
         if (a.res) {
+            float4 r[B][R][NI];
 #pragma unroll
             for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int m = 0; m < R; ++m)
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
-                        if (b * teams < have && in[i]) {
-                            float r[V];
-                            load_vec<kF32, V>(a.res, base + ((b * step + m) * a.C + TL * i * V), r);
-                            for (int k = 0; k < V; ++k) v[b][m][i][k] = as_stored<XT>(v[b][m][i][k] + r[k]);
-                        }
+                        r[b][m][i] = *reinterpret_cast<const float4*>(a.res + base + (off[b][i] + m * a.C));
 #pragma unroll
             for (int b = 0; b < B; ++b)
 #pragma unroll
                 for (int m = 0; m < R; ++m)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        if (b * teams < have && in[i])
-                            store_vec<XT, V>(a.sum, base + ((b * step + m) * a.C + TL * i * V), v[b][m][i]);
+                    for (int i = 0; i < NI; ++i) {
+                        float (&h)[V] = v[b][m][i];
+                        h[0] = as_stored<XT>(h[0] + r[b][m][i].x);
+                        h[1] = as_stored<XT>(h[1] + r[b][m][i].y);
+                        h[2] = as_stored<XT>(h[2] + r[b][m][i].z);
+                        h[3] = as_stored<XT>(h[3] + r[b][m][i].w);
+                        if (b * teams < have && in[i]) store_vec<XT, V>(a.sum, base + (off[b][i] + m * a.C), h);
+                    }
         }
         if (a.codes)
 #pragma unroll
@@ -60,9 +72,17 @@ __device__ __forceinline__ void norm_unit(const NormArgs& a, int64_t node0, int6
                 for (int m = 0; m < R; ++m)
 #pragma unroll
                     for (int i = 0; i < NI; ++i)
-                        store_codes<V>(a.codes, a.scales, row0 + b * step + m, a.C, a.nb, (t + TL * i) * V,
+                        store_codes<V>(a.codes, a.scales, row0 + row[b] + m, a.C, a.nb, (t + TL * i) * V,
                                        b * teams < have && in[i], TL, v[b][m][i]);
     }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+        if (!in[i])
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int m = 0; m < R; ++m)
+                    for (int k = 0; k < V; ++k) v[b][m][i][k] = 0.f;
     float mu[B], q[B];
     if constexpr (l == 0) {
 #pragma unroll
@@ -108,7 +128,7 @@ __device__ __forceinline__ void norm_unit(const NormArgs& a, int64_t node0, int6
                 if (b * teams < have) {
                     float y[V];
                     for (int k = 0; k < V; ++k) y[k] = v[b][m][i][k] * q[b] * w[k] + bias[k];
-                    store_vec<YT, V>(a.y, base + ((b * step + m) * a.C + TL * i * V), y);
+                    store_vec<YT, V>(a.y, base + (off[b][i] + m * a.C), y);
                 }
     }
     if (t == 0)
@@ -122,7 +142,7 @@ __device__ __forceinline__ void norm_unit(const NormArgs& a, int64_t node0, int6
 }
 
 template <int XT, int YT, int NI>
-__global__ void __launch_bounds__(256, NI == 1 ? 3 : 2) k_norm_teams(NormArgs a, int TL, int S, Units un) {
+__global__ void __launch_bounds__(256, NI == 1 ? 2 : 1) k_norm_teams(NormArgs a, int TL, int S, Units un) {
     const int teams = 32 / TL;
     const int64_t c0 = (int64_t)blockIdx.x * S, end = min(c0 + S, a.n);
     for (int u = threadIdx.x >> 5; u < un.total; u += 8) {

@@ -12,35 +12,44 @@ __device__ __forceinline__ void norm_bwd_unit(const NormBwdArgs& a, int64_t node
     constexpr int R = 2 * l + 1, B = nodes_of(l, bwd_rows(NI)), V = 4;
     const int lane = threadIdx.x & 31, t = lane & (TL - 1), teams = 32 / TL, K = (a.L + 1) * (a.L + 1);
     const int64_t first = node0 + lane / TL;
-    const int64_t row0 = first * K + l * l, base = row0 * a.C + t * V;
-    const int step = teams * K;
     const int have = (int)min((int64_t)B * teams, end - first);
-    bool in[NI];
-    float x[B][R][NI][V], g[B][R][NI][V], mu[B], r[B], s1[B], s2[B];
+    bool in[NI];  // unpredicated loads, as in the forward
+    int row[B], off[B][NI];
+    const int64_t node_at = min(first, end - 1), row0 = node_at * K + l * l, base = row0 * a.C;
 #pragma unroll
     for (int i = 0; i < NI; ++i) in[i] = (t + TL * i) * V < a.C;
 #pragma unroll
     for (int b = 0; b < B; ++b) {
+        row[b] = b * teams < have ? b * teams * K : 0;
 #pragma unroll
-        for (int m = 0; m < R; ++m)
+        for (int i = 0; i < NI; ++i) off[b][i] = row[b] * a.C + (in[i] ? (t + TL * i) * V : 0);
+    }
+    float x[B][R][NI][V], g[B][R][NI][V], mu[B], r[B], s1[B], s2[B];
+    {
+        Raw4<XT> raw[B][R][NI];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                for (int k = 0; k < V; ++k) x[b][m][i][k] = g[b][m][i][k] = 0.f;
-                if (b * teams < have && in[i]) {
-                    if constexpr (XT == kMXI8)
-                        load_codes<V>(static_cast<const int8_t*>(a.x), a.xs, row0 + b * step + m, a.C, a.nb,
-                                      (t + TL * i) * V, x[b][m][i]);
-                    else
-                        load_vec<XT, V>(a.x, base + ((b * step + m) * a.C + TL * i * V), x[b][m][i]);
-                    load_vec<kF32, V>(a.gy, base + ((b * step + m) * a.C + TL * i * V), g[b][m][i]);
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    raw[b][m][i].load(a.x, a.xs, base + (off[b][i] + m * a.C),
+                                      (row0 + row[b] + m) * a.nb + (in[i] ? (t + TL * i) * V / kCkBlock : 0));
+                    load_vec<kF32, V>(a.gy, base + (off[b][i] + m * a.C), g[b][m][i]);
                 }
-            }
-        mu[b] = r[b] = 0.f;
-        if (b * teams < have) {
-            if constexpr (l == 0) mu[b] = a.mean[first + b * teams];
-            r[b] = a.rstd[(first + b * teams) * (a.L + 1) + l];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int64_t node = node_at + (b * teams < have ? b * teams : 0);
+            mu[b] = l == 0 ? a.mean[node] : 0.f;
+            r[b] = a.rstd[node * (a.L + 1) + l];
+            s1[b] = s2[b] = 0.f;
         }
-        s1[b] = s2[b] = 0.f;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+#pragma unroll
+            for (int m = 0; m < R; ++m)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) raw[b][m][i].get(x[b][m][i]);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -84,7 +93,7 @@ __device__ __forceinline__ void norm_bwd_unit(const NormBwdArgs& a, int64_t node
 #pragma unroll
             for (int i = 0; i < NI; ++i)
                 if (b * teams < have && in[i]) {
-                    const int64_t at = base + ((b * step + m) * a.C + TL * i * V);
+                    const int64_t at = base + (off[b][i] + m * a.C);
                     float d[V];
                     for (int k = 0; k < V; ++k)
                         d[k] = r[b] * (g[b][m][i][k] - (l == 0 ? s1[b] : 0.f) - x[b][m][i][k] * s2[b]);
@@ -210,22 +219,22 @@ struct JoinPlan {
     int count[kMaxL + 2];
 };
 
-__global__ void __launch_bounds__(256) k_norm_join(const float* part, int L, int C, JoinPlan p, float* gw, float* gb) {
-    __shared__ float sh[8][33];
-    const int l = blockIdx.y, c = blockIdx.x * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
+__global__ void __launch_bounds__(1024) k_norm_join(const float* part, int L, int C, JoinPlan p, float* gw, float* gb) {
+    __shared__ float sh[32][33];
+    const int l = blockIdx.y, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, w = threadIdx.x >> 5;
     float* out = l <= L ? gw : gb;
     if (!out) return;
     const float* q = part + p.base[l] + c;
     float s = 0.f;
     if (c < C)
-#pragma unroll 4
-        for (int r = w; r < p.count[l]; r += 8) s += q[r * p.stride];
-    sh[w][threadIdx.x & 31] = s;
+#pragma unroll 10
+        for (int r = w; r < p.count[l]; r += 32) s += q[r * p.stride];
+    sh[w][lane] = s;
     __syncthreads();
-    if (w == 0 && c < C) {
-        for (int k = 1; k < 8; ++k) s += sh[k][threadIdx.x];
-        out[(l <= L ? (int64_t)l * C : 0) + c] = s;
-    }
+    s = sh[lane][w];  // warp w sums column w
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int cw = blockIdx.x * 32 + w;
+    if (lane == 0 && cw < C) out[(l <= L ? (int64_t)l * C : 0) + cw] = s;
 }
 
 template <int XT, int V>
@@ -283,7 +292,7 @@ cudaError_t launch_bwd(NormBwdArgs a, float* gw, float* gb, cudaStream_t s) {
     }
     if (e != cudaSuccess || !a.part) return e;
     count_launch();
-    k_norm_join<<<dim3((a.C + 31) / 32, a.L + 2), 256, 0, s>>>(a.part, a.L, a.C, j, gw, gb);
+    k_norm_join<<<dim3((a.C + 31) / 32, a.L + 2), 1024, 0, s>>>(a.part, a.L, a.C, j, gw, gb);
     return cudaGetLastError();
 }
 
