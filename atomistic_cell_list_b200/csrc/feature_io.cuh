@@ -69,24 +69,31 @@ __device__ __forceinline__ float ck_scale(uint32_t s) {
     return __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
 }
 
-// scale byte of a block from the largest magnitude bits in it: the exponent of
-// the largest value, at least 2^-120 so that the unit 2^(e-6) and its inverse
-// are normal numbers
-__device__ __forceinline__ uint32_t ck_byte(uint32_t max_bits) { return max(max_bits >> 23, 7u); }
+// scale byte of a block from its largest magnitude (NaN if any value is): the
+// exponent of the largest value, at least 2^-120 so that the unit 2^(e-6) and
+// its inverse are normal numbers
+__device__ __forceinline__ uint32_t ck_byte(float top) { return max(__float_as_uint(top) >> 23, 7u); }
 
-__device__ __forceinline__ uint32_t ck_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// code of v in a block of scale byte s: rint(v 2^(6-e)) clamped to +-127. The
-// scaling is a power of two, so the code does not depend on how it is computed.
-__device__ __forceinline__ int ck_code(float v, uint32_t s) {
-    if (s == 255u) return 0;
-    return min(127, max(-127, __float2int_rn(v * __uint_as_float((260u - s) << 23))));
+// the larger magnitude; a NaN on either side stays
+__device__ __forceinline__ float mag_max(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
 }
 
-// A code byte as fp32, without a conversion instruction: the byte with its sign
-// bit turned over is code + 128, placed in the low mantissa of 2^23.
-__device__ __forceinline__ float ck_value(uint32_t biased_byte) {
-    return __uint_as_float(0x4b000000u | biased_byte) - 8388736.f;
+// code of v in a block of scale byte s < 255: rint(v 2^(6-e)) clamped to +-127,
+// in the low byte. The scaling is a power of two and fma rounds once, to whole
+// numbers at 1.5 2^23 (half to even): the code does not depend on how it is computed.
+__device__ __forceinline__ uint32_t ck_code(float v, float inv) {
+    constexpr float kMagic = 12582912.f;
+    return __float_as_uint(fminf(fmaxf(fmaf(v, inv, kMagic), kMagic - 127.f), kMagic + 127.f));
+}
+__device__ __forceinline__ float ck_inverse(uint32_t s) { return __uint_as_float((260u - s) << 23); }
+
+// A code as fp32, without a conversion instruction: the byte with its sign bit
+// turned over is code + 128, placed (by a byte permutation) in the low mantissa of 2^23.
+__device__ __forceinline__ float ck_value(uint32_t biased, uint32_t select) {
+    return __uint_as_float(__byte_perm(biased, 0x4b000000u, select)) - 8388736.f;
 }
 
 // Four channels as storage keeps them, so that loads can be issued in a batch
@@ -96,6 +103,7 @@ struct Raw4;
 template <>
 struct Raw4<kF32> {
     float4 a;
+    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const float4*>(p); }
     __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
         a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     }
@@ -106,6 +114,7 @@ struct Raw4<kF32> {
 template <>
 struct Raw4<kBF16> {
     uint2 a;
+    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const uint2*>(p); }
     __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
         a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
@@ -117,6 +126,7 @@ struct Raw4<kBF16> {
 template <>
 struct Raw4<kMXI8> {
     uint32_t a, s;
+    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const uint32_t*>(p); }
     __device__ __forceinline__ void load(const void* p, const uint8_t* scales, int64_t i, int64_t block) {
         a = *reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(p) + i);
         s = scales[block];
@@ -124,8 +134,8 @@ struct Raw4<kMXI8> {
     __device__ __forceinline__ void get(float (&v)[4]) const {
         const float u = ck_scale(s) * 0.015625f;  // exact: at least 2^-133
         const uint32_t b = a ^ 0x80808080u;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = ck_value((b >> (8 * k)) & 255u) * u;
+        v[0] = ck_value(b, 0x7650) * u; v[1] = ck_value(b, 0x7651) * u;
+        v[2] = ck_value(b, 0x7652) * u; v[3] = ck_value(b, 0x7653) * u;
     }
 };
 
@@ -155,27 +165,26 @@ __device__ __forceinline__ void load_feat(const void* p, const uint8_t* s, int64
 }
 
 // Checkpoint of V channels per lane, lanes in channel order: a block of 32
-// channels is 32/V lanes (of one team of `team` lanes, when rows are shorter).
-// Every lane of the warp calls it; lanes beyond the row pass ok = false.
+// channels is 32/V lanes, fewer when the lanes of a row (`team`) are fewer.
+// Every lane of the warp calls it; lanes beyond the row pass zeros and ok = false.
 template <int V>
 __device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int64_t row, int C, int nb, int c, bool ok,
                                             int team, const float (&v)[V]) {
-    uint32_t m = 0;
-    if (ok)
-        for (int k = 0; k < V; ++k) m = max(m, ck_mag(v[k]));
+    float m = fabsf(v[0]);
+    for (int k = 1; k < V; ++k) m = mag_max(m, v[k]);
     constexpr int G = kCkBlock / V;
     for (int o = 1; o < G; o <<= 1)
-        if (o < team) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (o < team) m = mag_max(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (!ok) return;
     const uint32_t s = ck_byte(m);
+    const float inv = ck_inverse(s);
     int8_t* q = codes + row * C + c;
     if constexpr (V == 4) {
-        char4 a;
-        a.x = (signed char)ck_code(v[0], s); a.y = (signed char)ck_code(v[1], s);
-        a.z = (signed char)ck_code(v[2], s); a.w = (signed char)ck_code(v[3], s);
-        *reinterpret_cast<char4*>(q) = a;
+        const uint32_t lo = __byte_perm(ck_code(v[0], inv), ck_code(v[1], inv), 0x0040);
+        const uint32_t hi = __byte_perm(ck_code(v[2], inv), ck_code(v[3], inv), 0x0040);
+        *reinterpret_cast<uint32_t*>(q) = s == 255u ? 0u : __byte_perm(lo, hi, 0x5410);
     } else {
-        for (int k = 0; k < V; ++k) q[k] = (int8_t)ck_code(v[k], s);
+        for (int k = 0; k < V; ++k) q[k] = s == 255u ? 0 : (int8_t)ck_code(v[k], inv);
     }
     if (c % kCkBlock == 0) scales[row * nb + c / kCkBlock] = (uint8_t)s;
 }

@@ -4,159 +4,162 @@
 namespace e2f {
 namespace {
 
+constexpr int kFwdWarps = 8;  // of a block, at 128 registers
+
+// the units of degree l that this block takes
 template <int XT, int YT, int NI, int l>
-__device__ __forceinline__ void norm_unit(const NormArgs& a, int64_t node0, int64_t end, int TL) {
-    constexpr int R = 2 * l + 1, B = nodes_of(l, fwd_rows(NI)), V = 4;
-    const int lane = threadIdx.x & 31, t = lane & (TL - 1), teams = 32 / TL, K = (a.L + 1) * (a.L + 1);
-    const int64_t first = node0 + lane / TL;  // a warp's teams take every `teams`-th node
-    const int have = (int)min((int64_t)B * teams, end - first);  // node b exists: b teams < have
-    // loads are not predicated: a missing node reads the chunk's last one, a lane beyond the row its first
-    // channels, so that all of a unit's loads are in flight at once
+__device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slots& sl, char* smem) {
+    using U = Unit<NI, l>;
+    constexpr int V = 4, E = vec_bytes<XT>() / 4, R = U::R, B = U::B;  // E: bytes of a value
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, t = lane & (TL - 1), C = a.C;
+    const int K = (a.L + 1) * (a.L + 1), teams = 32 / TL, team0 = lane / TL * (B * R);
+    const char* zeros = smem + warps * sl.stages * sl.stage_bytes;  // what lanes beyond the row read
+    const char* mine = smem + warp * sl.stages * sl.stage_bytes;
+    const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+    int c[NI];
     bool in[NI];
-    int row[B], off[B][NI];
-    const int64_t row0 = min(first, end - 1) * K + l * l, base = row0 * a.C;
+    float w[NI][V], bias[NI][V] = {};
 #pragma unroll
-    for (int i = 0; i < NI; ++i) in[i] = (t + TL * i) * V < a.C;
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-        row[b] = b * teams < have ? b * teams * K : 0;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) off[b][i] = row[b] * a.C + (in[i] ? (t + TL * i) * V : 0);
+    for (int i = 0; i < NI; ++i) {
+        in[i] = (t + TL * i) * V < C;
+        c[i] = in[i] ? (t + TL * i) * V : 0;
+        load_vec<kF32, V>(a.w, l * C + c[i], w[i]);
+        if (l == 0 && a.b) load_vec<kF32, V>(a.b, c[i], bias[i]);
     }
-    float v[B][R][NI][V];
-    {
-        Raw4<XT> raw[B][R][NI];
+    const int blocks = sl.at[l + 1] - sl.at[l];
+    const int64_t step = (int64_t)blocks * warps, units = (a.n + B * teams - 1) / (B * teams);
+    int64_t k = (int)blockIdx.x - sl.at[l] + (int64_t)blocks * warp;
+    auto fetch = [&](int64_t k, int stage) {
+        if (k < units) {
+            const U u(k, a.n, K, TL);
+            const uint32_t to = mine_s + stage * sl.stage_bytes;
+            u.template fetch<XT>(a.x, C, K, TL, to);
+            if (XT != kMXI8 && a.res) u.template fetch<kF32>(a.res, C, K, TL, to + sl.o1);
+        }
+        cp_commit();
+    };
+    uint32_t scale[B * R][NI] = {}, next[B * R][NI] = {};  // of the unit in work and of the next one, where x has any
+    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+    for (int s = 0; s + 1 < sl.stages; ++s) fetch(k + s * step, s);
+    for (int s = 0; k < units; k += step, s = s + 1 == sl.stages ? 0 : s + 1) {
+        const U u(k, a.n, K, TL);
+        __syncwarp();  // the whole warp is done with the stage that is filled next
+        fetch(k + (sl.stages - 1) * step, s == 0 ? sl.stages - 1 : s - 1);
+        if constexpr (XT == kMXI8) {
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+            for (int m = 0; m < B * R; ++m)
+#pragma unroll
+                for (int i = 0; i < NI; ++i) scale[m][i] = next[m][i];
+            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+        }
+        cp_wait(sl.stages - 1);
+        __syncwarp();
+        const char* st = mine + s * sl.stage_bytes;
+        const int64_t base = u.row0 * C;
+        float v[B][R][NI][V];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const char* p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
+            const int pitch = in[i] ? C * E : 0;
+#pragma unroll
+            for (int b = 0; b < B; ++b)
+#pragma unroll
+                for (int m = 0; m < R; ++m) {
+                    Raw4<XT> raw;
+                    raw.from(p + (b * R + m) * pitch);
+                    if constexpr (XT == kMXI8) raw.s = scale[b * R + m][i];
+                    raw.get(v[b][m][i]);
+                }
+            if constexpr (XT != kMXI8) {
+                if (a.res) {
+                    const char* r = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
+                    const int r_pitch = in[i] ? C * 4 : 0;
+#pragma unroll
+                    for (int b = 0; b < B; ++b)
+#pragma unroll
+                        for (int m = 0; m < R; ++m) {
+                            const float4 e = *reinterpret_cast<const float4*>(r + (b * R + m) * r_pitch);
+                            float (&h)[V] = v[b][m][i];
+                            h[0] = as_stored<XT>(h[0] + e.x); h[1] = as_stored<XT>(h[1] + e.y);
+                            h[2] = as_stored<XT>(h[2] + e.z); h[3] = as_stored<XT>(h[3] + e.w);
+                            if (b < u.have && in[i])
+                                store_vec<XT, V>(a.sum, base + ((b * teams * K + m) * C + c[i]), h);
+                        }
+                }
+                if (a.codes)
+#pragma unroll
+                    for (int b = 0; b < B; ++b)
+#pragma unroll
+                        for (int m = 0; m < R; ++m)
+                            store_codes<V>(a.codes, a.scales, u.row0 + (b * teams * K + m), C, a.nb, c[i],
+                                           b < u.have && in[i], TL, v[b][m][i]);
+            }
+        }
+        float mu[B], q[B];
+        if constexpr (l == 0) {
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                mu[b] = 0.f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    for (int k = 0; k < V; ++k) mu[b] += v[b][0][i][k];
+            }
+            team_sum(mu, TL);
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                mu[b] *= a.inv_c;
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    for (int k = 0; k < V; ++k) v[b][0][i][k] -= in[i] ? mu[b] : 0.f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            q[b] = 0.f;
 #pragma unroll
             for (int m = 0; m < R; ++m)
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    raw[b][m][i].load(a.x, a.xs, base + (off[b][i] + m * a.C),
-                                      (row0 + row[b] + m) * a.nb + (in[i] ? (t + TL * i) * V / kCkBlock : 0));
+                    for (int k = 0; k < V; ++k) q[b] += v[b][m][i][k] * v[b][m][i][k];
+        }
+        team_sum(q, TL);
 #pragma unroll
-        for (int b = 0; b < B; ++b)
+        for (int b = 0; b < B; ++b) {
+            q[b] = rsqrtf(q[b] * (a.inv_c * (1.f / R)) + a.eps);
 #pragma unroll
-            for (int m = 0; m < R; ++m)
+            for (int i = 0; i < NI; ++i) {
+                float f[V];
+                for (int k = 0; k < V; ++k) f[k] = q[b] * w[i][k];
+                if (b < u.have && in[i])
 #pragma unroll
-                for (int i = 0; i < NI; ++i) raw[b][m][i].get(v[b][m][i]);
-    }
-    if constexpr (XT != kMXI8) {
-        if (a.res) {
-            float4 r[B][R][NI];
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int m = 0; m < R; ++m)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        r[b][m][i] = *reinterpret_cast<const float4*>(a.res + base + (off[b][i] + m * a.C));
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int m = 0; m < R; ++m)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        float (&h)[V] = v[b][m][i];
-                        h[0] = as_stored<XT>(h[0] + r[b][m][i].x);
-                        h[1] = as_stored<XT>(h[1] + r[b][m][i].y);
-                        h[2] = as_stored<XT>(h[2] + r[b][m][i].z);
-                        h[3] = as_stored<XT>(h[3] + r[b][m][i].w);
-                        if (b * teams < have && in[i]) store_vec<XT, V>(a.sum, base + (off[b][i] + m * a.C), h);
+                    for (int m = 0; m < R; ++m) {
+                        float y[V];
+                        for (int k = 0; k < V; ++k)
+                            y[k] = l == 0 ? fmaf(v[b][m][i][k], f[k], bias[i][k]) : v[b][m][i][k] * f[k];
+                        store_vec<YT, V>(a.y, base + ((b * teams * K + m) * C + c[i]), y);
                     }
-        }
-        if (a.codes)
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int m = 0; m < R; ++m)
-#pragma unroll
-                    for (int i = 0; i < NI; ++i)
-                        store_codes<V>(a.codes, a.scales, row0 + row[b] + m, a.C, a.nb, (t + TL * i) * V,
-                                       b * teams < have && in[i], TL, v[b][m][i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i)
-        if (!in[i])
-#pragma unroll
-            for (int b = 0; b < B; ++b)
-#pragma unroll
-                for (int m = 0; m < R; ++m)
-                    for (int k = 0; k < V; ++k) v[b][m][i][k] = 0.f;
-    float mu[B], q[B];
-    if constexpr (l == 0) {
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            mu[b] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                for (int k = 0; k < V; ++k) mu[b] += v[b][0][i][k];
-        }
-        team_sum(mu, TL);
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            mu[b] /= a.C;
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (in[i])
-                    for (int k = 0; k < V; ++k) v[b][0][i][k] -= mu[b];
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-        q[b] = 0.f;
-#pragma unroll
-        for (int m = 0; m < R; ++m)
-#pragma unroll
-            for (int i = 0; i < NI; ++i)
-                for (int k = 0; k < V; ++k) q[b] += v[b][m][i][k] * v[b][m][i][k];
-    }
-    team_sum(q, TL);
-#pragma unroll
-    for (int b = 0; b < B; ++b) q[b] = 1.f / sqrtf(q[b] / ((float)R * a.C) + a.eps);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        if (!in[i]) continue;
-        const int c = (t + TL * i) * V;
-        float w[V], bias[V] = {};
-        load_vec<kF32, V>(a.w, l * a.C + c, w);
-        if (l == 0 && a.b) load_vec<kF32, V>(a.b, c, bias);
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-#pragma unroll
-            for (int m = 0; m < R; ++m)
-                if (b * teams < have) {
-                    float y[V];
-                    for (int k = 0; k < V; ++k) y[k] = v[b][m][i][k] * q[b] * w[k] + bias[k];
-                    store_vec<YT, V>(a.y, base + (off[b][i] + m * a.C), y);
-                }
-    }
-    if (t == 0)
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (b * teams < have) {
-                const int64_t node = first + b * teams;
+            }
+            if (t == 0 && b < u.have) {
+                const int64_t node = u.first + b * teams;
                 if (l == 0 && a.mean) a.mean[node] = mu[b];
                 if (a.rstd) a.rstd[node * (a.L + 1) + l] = q[b];
             }
+        }
+    }
 }
 
 template <int XT, int YT, int NI>
-__global__ void __launch_bounds__(256, NI == 1 ? 2 : 1) k_norm_teams(NormArgs a, int TL, int S, Units un) {
-    const int teams = 32 / TL;
-    const int64_t c0 = (int64_t)blockIdx.x * S, end = min(c0 + S, a.n);
-    for (int u = threadIdx.x >> 5; u < un.total; u += 8) {
-        int j = u, l = kMaxL;  // the largest degrees first
-        while (j >= un.n[l]) j -= un.n[l--];
-        j *= teams;
-        switch (l) {
-            case 0: norm_unit<XT, YT, NI, 0>(a, c0 + j * nodes_of(0, fwd_rows(NI)), end, TL); break;
-            case 1: norm_unit<XT, YT, NI, 1>(a, c0 + j * nodes_of(1, fwd_rows(NI)), end, TL); break;
-            case 2: norm_unit<XT, YT, NI, 2>(a, c0 + j * nodes_of(2, fwd_rows(NI)), end, TL); break;
-            case 3: norm_unit<XT, YT, NI, 3>(a, c0 + j * nodes_of(3, fwd_rows(NI)), end, TL); break;
-            default: norm_unit<XT, YT, NI, 4>(a, c0 + j * nodes_of(4, fwd_rows(NI)), end, TL); break;
-        }
-    }
+__global__ void __launch_bounds__(32 * kFwdWarps, 2) k_norm_teams(NormArgs a, int TL, Slots sl) {
+    extern __shared__ __align__(16) char smem[];
+    if (threadIdx.x < 16)
+        reinterpret_cast<float*>(smem + (blockDim.x >> 5) * sl.stages * sl.stage_bytes)[threadIdx.x] = 0.f;
+    __syncthreads();
+    const int blk = blockIdx.x;
+    if (blk < sl.at[1]) norm_degree<XT, YT, NI, 0>(a, TL, sl, smem);
+    else if (blk < sl.at[2]) norm_degree<XT, YT, NI, 1>(a, TL, sl, smem);
+    else if (blk < sl.at[3]) norm_degree<XT, YT, NI, 2>(a, TL, sl, smem);
+    else if (blk < sl.at[4]) norm_degree<XT, YT, NI, 3>(a, TL, sl, smem);
+    else norm_degree<XT, YT, NI, 4>(a, TL, sl, smem);
 }
 
 // One block per (node, degree); any C.
@@ -218,14 +221,23 @@ __global__ void k_norm_rows(NormArgs a) {
     }
 }
 
+template <int XT, int YT, int NI>
+cudaError_t launch_teams(const NormArgs& a, const TeamPlan& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(k_norm_teams<XT, YT, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem);
+    if (e != cudaSuccess) return e;
+    Slots sl{p.stage_bytes, p.stages, kUnitRows * NI * 32 * vec_bytes<XT>(), 0, 0, {}};
+    std::copy(p.at, p.at + kMaxL + 2, sl.at);
+    k_norm_teams<XT, YT, NI><<<p.at[kMaxL + 1], 32 * p.warps, p.smem, s>>>(a, p.TL, sl);
+    return cudaGetLastError();
+}
+
 template <int XT, int YT>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
     count_launch();
     if (use_teams(a.C)) {
-        const TeamPlan p = team_plan(a.n, a.L, a.C, 4 * kSMs, true);
-        if (p.NI == 1) k_norm_teams<XT, YT, 1><<<(unsigned)p.chunks, 256, 0, s>>>(a, p.TL, p.S, p.un);
-        else k_norm_teams<XT, YT, 2><<<(unsigned)p.chunks, 256, 0, s>>>(a, p.TL, p.S, p.un);
-        return cudaGetLastError();
+        const int vec = vec_bytes<XT>() + (a.res ? 16 : 0);
+        const TeamPlan p = team_plan(a.n, a.L, a.C, vec, vec, 0, kFwdWarps);
+        return p.NI == 1 ? launch_teams<XT, YT, 1>(a, p, s) : launch_teams<XT, YT, 2>(a, p, s);
     }
     const unsigned grid = (unsigned)std::min<int64_t>(a.n * (a.L + 1), 1 << 20);
     if (a.C % 4 == 0) k_norm_rows<XT, YT, 4><<<grid, row_threads(a.C, 4), 0, s>>>(a);
@@ -259,7 +271,7 @@ extern "C" e2f_status e2f_layer_norm(const e2f_norm_cfg* cfg, int64_t n_atoms, c
     if (misaligned(x) || misaligned(residual) || misaligned(weight) || misaligned(bias) || misaligned(sum) ||
         misaligned(y) || misaligned(ck_codes))
         return E2F_ERR_ALIGNMENT;
-    NormArgs a{n_atoms, cfg->L, cfg->C, ck_blocks(cfg->C), cfg->eps, x,    x_scales, residual,
+    NormArgs a{n_atoms, cfg->L, cfg->C, ck_blocks(cfg->C), cfg->eps, 1.f / cfg->C, x, x_scales, residual,
                sum,     weight, bias,   y,                 mean,     rstd, ck_codes, ck_scales};
     cudaStream_t s = static_cast<cudaStream_t>(stream_);
     const bool yb = cfg->y_dtype == E2F_BF16;

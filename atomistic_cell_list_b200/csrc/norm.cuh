@@ -9,13 +9,17 @@
 //   grad_weight[l,c] = sum_{n,m} grad_y xh,   grad_bias[c] = sum_n grad_y[n,0,c]
 // All sums are fp32. A few operations per value: memory bound.
 //
-// C a multiple of 4 up to 256: a team of lanes per row, everything in
-// registers, one pass over the data. A team of TL lanes (a power of two,
-// TL >= C/4 up to 32) owns whole rows: lane t holds channels 4 (t + TL i) .. +3,
-// i < NI, of all 2l+1 rows of a group, and of B nodes at once where groups are
-// small, so that 6 to 10 row loads are in flight per lane at every degree
-// (NI = 1). Sums are shuffles. Chunks of S nodes with all their degrees keep a
-// chunk's rows close in time and in address.
+// C a multiple of 16 up to 256 (what the attention takes): a team of TL lanes (a
+// power of two, TL >= C/4 up to 32) owns whole rows, lane t the channels
+// 4 (t + TL i) .. +3, i < NI. A block works on one degree, so that its code has the
+// rows of a group unrolled and stays in the instruction cache (with all degrees in
+// every block the warps waited for instructions; with one code for all degrees
+// they executed twice as many). One warp takes a unit: as many nodes per team as
+// make 5 to 9 rows, held in registers. A (node, degree) group is contiguous in
+// memory: its team copies it in 16-byte pieces (cp.async) to the warp's own part of
+// shared memory, one to three units ahead of the one in work. Warps never wait for
+// one another, and the bytes in flight (about 100 KB an SM) do not depend on
+// registers or occupancy. Lanes beyond the row read zeros.
 // Any other C: one block per (node, degree).
 #pragma once
 
@@ -37,7 +41,7 @@ constexpr int kNormBlocks = 592;  // most blocks of a weight-gradient pass: 4 on
 struct NormArgs {
     int64_t n;
     int L, C, nb;
-    float eps;
+    float eps, inv_c;
     const void* x;
     const uint8_t* xs;
     const float* res;
@@ -54,6 +58,7 @@ struct NormArgs {
 struct NormBwdArgs {
     int64_t n;
     int L, C, nb;
+    float inv_c;
     const void* x;
     const uint8_t* xs;
     const float* w;
@@ -69,42 +74,113 @@ struct NormBwdArgs {
 constexpr int kSMs = 148;
 constexpr int kTeamC = 256;  // most channels a team holds
 
-// nodes of degree l that a team takes at once, to have about `rows` rows in its registers
-constexpr int nodes_of(int l, int rows) { return rows / (2 * l + 1) < 1 ? 1 : rows / (2 * l + 1); }
-// the backward holds x and grad_y: fewer rows, within 128 registers at NI = 1
-constexpr int fwd_rows(int NI) { return NI == 1 ? 9 : 5; }
-constexpr int bwd_rows(int NI) { return NI == 1 ? 6 : 3; }
+constexpr int kUnitRows = 9;  // most rows of a unit per team
+constexpr int kBlockSmem = 113 * 1024;  // two blocks per SM
+constexpr int kTeamBlocks = 2 * kSMs;
 
-struct Units {  // units (one warp, one degree, B nodes per team) of a chunk of S nodes
-    int n[kMaxL + 1], total;
-};
+// nodes of degree l that a team takes at once
+__host__ __device__ constexpr int unit_nodes(int l) { return l == 0 ? 9 : l == 1 ? 3 : 1; }
 
+// The blocks [at[l], at[l+1]) work on degree l.
 struct TeamPlan {
-    int NI, TL, S;
-    int64_t chunks;
-    Units un;
+    int NI, TL, warps, stages, stage_bytes;  // stages: units per warp in flight or in work
+    int at[kMaxL + 2];
+    size_t smem;
 };
 
-bool use_teams(int C) { return C % 4 == 0 && C <= kTeamC; }
+// where the second and third stream and the statistics of a unit lie in a stage
+struct Slots {
+    int stage_bytes, stages, o1, o2, o3, at[kMaxL + 2];
+};
 
-// Lanes and chunk size for n nodes: chunks of 24 nodes a team (whole units at
-// every degree), fewer when that gives less than `blocks` chunks.
-TeamPlan team_plan(int64_t n, int L, int C, int blocks, bool fwd) {
+bool use_teams(int C) { return C % 16 == 0 && C <= kTeamC; }
+
+// bytes of 4 channels
+template <int T>
+constexpr int vec_bytes() { return T == kF32 ? 16 : T == kBF16 ? 8 : 4; }
+
+// Plan of n nodes whose units read `vec` bytes per lane and vector of 4 channels
+// (`most` with every optional input) and `small` more bytes per stage. As many
+// warps as a block's shared memory gives two stages of `most`, up to `cap` (by
+// registers), then up to 4 stages: which warp takes which unit, and so the order of
+// the weight gradient's sums, does not depend on the optional inputs. Degrees get
+// blocks by their rows, with half a row more for a group's sums.
+TeamPlan team_plan(int64_t n, int L, int C, int vec, int most, int small, int cap) {
     TeamPlan p{};
-    p.TL = 1;
+    p.TL = 4;
     while (p.TL < 32 && p.TL * 4 < C) p.TL *= 2;
     p.NI = p.TL * 4 < C ? 2 : 1;
-    const int teams = 32 / p.TL;
-    p.S = 24 * teams;
-    while (p.S > 1 && (n + p.S - 1) / p.S < blocks) p.S = (p.S + 1) / 2;
-    p.chunks = (n + p.S - 1) / p.S;
+    const int row = kUnitRows * p.NI * 32;
+    p.stage_bytes = row * vec + small;
+    p.warps = std::min(cap, (kBlockSmem - 64) / (2 * (row * most + small)));
+    p.stages = std::min(4, (kBlockSmem - 64) / p.warps / p.stage_bytes);
+    p.smem = (size_t)p.warps * p.stages * p.stage_bytes + 64;
+    const double rows = (L + 1) * (L + 1) + 0.5 * (L + 1);
     for (int l = 0; l <= L; ++l) {
-        const int per = nodes_of(l, fwd ? fwd_rows(p.NI) : bwd_rows(p.NI)) * teams;
-        p.un.n[l] = (p.S + per - 1) / per;
-        p.un.total += p.un.n[l];
+        const int64_t units = (n + unit_nodes(l) * (32 / p.TL) - 1) / (unit_nodes(l) * (32 / p.TL));
+        const int share = std::max(1, (int)(kTeamBlocks * (2 * l + 1.5) / rows));
+        p.at[l + 1] = p.at[l] + (int)std::min<int64_t>(share, units);
     }
+    for (int l = L + 1; l <= kMaxL; ++l) p.at[l + 1] = p.at[l];
     return p;
 }
+
+__device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// all but the newest n groups of this thread have arrived
+__device__ __forceinline__ void cp_wait(int n) {
+    if (n <= 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else asm volatile("cp.async.wait_group 3;" ::: "memory");
+}
+
+// A lane's view of unit k of degree l, B nodes per team: first, first + teams, ...
+template <int NI, int l>
+struct Unit {
+    static constexpr int R = 2 * l + 1, B = unit_nodes(l);
+    int64_t first, row0;
+    int have;  // node b exists: b < have
+    __device__ __forceinline__ Unit(int64_t k, int64_t n, int K, int TL) {
+        const int teams = 32 / TL;
+        first = k * (B * teams) + (threadIdx.x & 31) / TL;
+        row0 = first * K + l * l;
+        const int64_t left = n - first;
+        have = left <= 0 ? 0 : left >= B * teams ? B : (int)(left + teams - 1) / teams;
+    }
+    // starts the copies of one stream [rows, C] of storage T to `to`: [team][node][row][C]
+    template <int T>
+    __device__ __forceinline__ void fetch(const void* p, int C, int K, int TL, uint32_t to) const {
+        constexpr int IT = (R * NI * vec_bytes<T>() + 15) / 16;
+        const int lane = threadIdx.x & 31, t16 = (lane & (TL - 1)) * 16, bytes = R * C * (vec_bytes<T>() / 4);
+        const char* q = static_cast<const char*>(p) + row0 * C * (vec_bytes<T>() / 4) + t16;
+        to += lane / TL * (B * bytes) + t16;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (b < have) {
+#pragma unroll
+                for (int j = 0; j < IT; ++j)
+                    if (t16 + j * TL * 16 < bytes) cp_async16(to + (b * bytes + j * TL * 16), q + j * TL * 16);
+                q += (int64_t)(32 / TL * K) * C * (vec_bytes<T>() / 4);
+            }
+    }
+    // scale bytes of a checkpoint's vectors, one lane's
+    __device__ __forceinline__ void scales(const uint8_t* xs, int nb, int K, int TL, const int (&c)[NI],
+                                           uint32_t (&s)[B * R][NI]) const {
+        const uint8_t* q = xs + row0 * nb;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (b < have)
+#pragma unroll
+                for (int m = 0; m < R; ++m)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) s[b * R + m][i] = q[(b * (32 / TL * K) + m) * nb + c[i] / kCkBlock];
+    }
+};
 
 template <int N>
 __device__ __forceinline__ void team_sum(float (&v)[N], int TL) {

@@ -4,146 +4,159 @@
 namespace e2f {
 namespace {
 
-constexpr int kBwdBlocks = 2 * kSMs;  // resident blocks of k_norm_bwd_teams
+constexpr int kBwdWarps = 4;  // of a block, at 255 registers: x and grad_y of a unit
+constexpr int kStatNodes = 72;  // most nodes of a unit: 9 for each of 8 teams
+constexpr int kStatBytes = 8 * kStatNodes;
 
-// acc: this lane's weight gradient of its channels, [degree or bias][NI] float4 with a stride of 32 float4
+// The units of degree l that this block takes. Each lane keeps the weight
+// gradient of its channels in registers until the end, then the block's lanes
+// that share channels are added in order: no atomics. part: [block][C], then
+// [block of degree 0][C] for the bias.
 template <int XT, int NI, int l>
-__device__ __forceinline__ void norm_bwd_unit(const NormBwdArgs& a, int64_t node0, int64_t end, int TL, float4* acc) {
-    constexpr int R = 2 * l + 1, B = nodes_of(l, bwd_rows(NI)), V = 4;
-    const int lane = threadIdx.x & 31, t = lane & (TL - 1), teams = 32 / TL, K = (a.L + 1) * (a.L + 1);
-    const int64_t first = node0 + lane / TL;
-    const int have = (int)min((int64_t)B * teams, end - first);
-    bool in[NI];  // unpredicated loads, as in the forward
-    int row[B], off[B][NI];
-    const int64_t node_at = min(first, end - 1), row0 = node_at * K + l * l, base = row0 * a.C;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) in[i] = (t + TL * i) * V < a.C;
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-        row[b] = b * teams < have ? b * teams * K : 0;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) off[b][i] = row[b] * a.C + (in[i] ? (t + TL * i) * V : 0);
-    }
-    float x[B][R][NI][V], g[B][R][NI][V], mu[B], r[B], s1[B], s2[B];
-    {
-        Raw4<XT> raw[B][R][NI];
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-#pragma unroll
-            for (int m = 0; m < R; ++m)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    raw[b][m][i].load(a.x, a.xs, base + (off[b][i] + m * a.C),
-                                      (row0 + row[b] + m) * a.nb + (in[i] ? (t + TL * i) * V / kCkBlock : 0));
-                    load_vec<kF32, V>(a.gy, base + (off[b][i] + m * a.C), g[b][m][i]);
-                }
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const int64_t node = node_at + (b * teams < have ? b * teams : 0);
-            mu[b] = l == 0 ? a.mean[node] : 0.f;
-            r[b] = a.rstd[node * (a.L + 1) + l];
-            s1[b] = s2[b] = 0.f;
-        }
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-#pragma unroll
-            for (int m = 0; m < R; ++m)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) raw[b][m][i].get(x[b][m][i]);
-    }
+__device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, const Slots& sl, char* smem) {
+    using U = Unit<NI, l>;
+    constexpr int V = 4, E = vec_bytes<XT>() / 4, R = U::R, B = U::B;
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, t = lane & (TL - 1), C = a.C;
+    const int K = (a.L + 1) * (a.L + 1), teams = 32 / TL, team = lane / TL, team0 = team * (B * R);
+    const char* zeros = smem + warps * sl.stages * sl.stage_bytes;
+    const char* mine = smem + warp * sl.stages * sl.stage_bytes;
+    const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+    int c[NI];
+    bool in[NI];
+    float w[NI][V], dw[NI][V] = {}, db[NI][V] = {};
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        if (!in[i]) continue;
-        float w[V], dw[V] = {}, db[V] = {};
-        load_vec<kF32, V>(a.w, l * a.C + (t + TL * i) * V, w);
-#pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (b * teams < have)
-#pragma unroll
-                for (int m = 0; m < R; ++m)
-                    for (int k = 0; k < V; ++k) {
-                        const float gk = g[b][m][i][k], u = gk * w[k];
-                        const float xh = (l == 0 ? x[b][m][i][k] - mu[b] : x[b][m][i][k]) * r[b];
-                        dw[k] += gk * xh;
-                        s2[b] += u * xh;
-                        if constexpr (l == 0) {
-                            db[k] += gk;
-                            s1[b] += u;
-                        }
-                        x[b][m][i][k] = xh;
-                        g[b][m][i][k] = u;
-                    }
-        if (a.part) {
-            float4& o = acc[(l * NI + i) * 32];
-            o = make_float4(o.x + dw[0], o.y + dw[1], o.z + dw[2], o.w + dw[3]);
-            if constexpr (l == 0) {
-                float4& p = acc[((a.L + 1) * NI + i) * 32];
-                p = make_float4(p.x + db[0], p.y + db[1], p.z + db[2], p.w + db[3]);
+        in[i] = (t + TL * i) * V < C;
+        c[i] = in[i] ? (t + TL * i) * V : 0;
+        load_vec<kF32, V>(a.w, l * C + c[i], w[i]);
+    }
+    const int blocks = sl.at[l + 1] - sl.at[l];
+    const int64_t step = (int64_t)blocks * warps, units = (a.n + B * teams - 1) / (B * teams);
+    int64_t k = (int)blockIdx.x - sl.at[l] + (int64_t)blocks * warp;
+    auto fetch = [&](int64_t k, int stage) {
+        if (k < units) {
+            const U u(k, a.n, K, TL);
+            uint32_t to = mine_s + stage * sl.stage_bytes;
+            u.template fetch<XT>(a.x, C, K, TL, to);
+            u.template fetch<kF32>(a.gy, C, K, TL, to + sl.o1);
+            if (a.skip) u.template fetch<kF32>(a.skip, C, K, TL, to + sl.o2);
+            to += sl.o3 + 4 * team * B;  // statistics: [team][node] rstd, then mean
+            for (int b = t; b < u.have; b += TL) {
+                const int64_t node = u.first + b * teams;
+                cp_async4(to + 4 * b, a.rstd + node * (a.L + 1) + l);
+                if (l == 0) cp_async4(to + 4 * (kStatNodes + b), a.mean + node);
             }
         }
-    }
-    if constexpr (l == 0) team_sum(s1, TL);
-    team_sum(s2, TL);
+        cp_commit();
+    };
+    uint32_t scale[B * R][NI] = {}, next[B * R][NI] = {};
+    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+    for (int s = 0; s + 1 < sl.stages; ++s) fetch(k + s * step, s);
+    for (int s = 0; k < units; k += step, s = s + 1 == sl.stages ? 0 : s + 1) {
+        const U u(k, a.n, K, TL);
+        __syncwarp();  // the whole warp is done with the stage that is filled next
+        fetch(k + (sl.stages - 1) * step, s == 0 ? sl.stages - 1 : s - 1);
+        if constexpr (XT == kMXI8) {
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-        s1[b] /= a.C;
-        s2[b] /= (float)R * a.C;
+            for (int m = 0; m < B * R; ++m)
 #pragma unroll
-        for (int m = 0; m < R; ++m)
+                for (int i = 0; i < NI; ++i) scale[m][i] = next[m][i];
+            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+        }
+        cp_wait(sl.stages - 1);
+        __syncwarp();
+        const char* st = mine + s * sl.stage_bytes;
+        const float* stat = reinterpret_cast<const float*>(st + sl.o3) + team * B;
+        float x[B][R][NI][V], g[B][R][NI][V], r[B], s1[B], s2[B];  // x becomes xh, g becomes u = grad_y weight
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            r[b] = stat[b];
+            s1[b] = s2[b] = 0.f;
+            const float mu = l == 0 ? stat[kStatNodes + b] : 0.f;
+            const bool ok = b < u.have;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const char* p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
+                const char* pg = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
+                const int pitch = in[i] ? C : 0;
+#pragma unroll
+                for (int m = 0; m < R; ++m) {
+                    float (&xv)[V] = x[b][m][i];
+                    Raw4<XT> raw;
+                    raw.from(p + (b * R + m) * pitch * E);
+                    if constexpr (XT == kMXI8) raw.s = scale[b * R + m][i];
+                    raw.get(xv);
+                    const float4 e = *reinterpret_cast<const float4*>(pg + (b * R + m) * pitch * 4);
+                    const float gv[V] = {e.x, e.y, e.z, e.w};
+                    for (int k = 0; k < V; ++k) {
+                        const float xh = (l == 0 ? xv[k] - mu : xv[k]) * r[b], uk = gv[k] * w[i][k];
+                        if (ok) dw[i][k] += gv[k] * xh;
+                        s2[b] += uk * xh;
+                        if constexpr (l == 0) {
+                            if (ok) db[i][k] += gv[k];
+                            s1[b] += uk;
+                        }
+                        xv[k] = xh;
+                        g[b][m][i][k] = uk;
+                    }
+                }
+            }
+        }
+        if constexpr (l == 0) team_sum(s1, TL);
+        team_sum(s2, TL);
+        const int64_t base = u.row0 * C;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const float m1 = s1[b] * a.inv_c * r[b], m2 = s2[b] * (a.inv_c * (1.f / R)) * r[b];
 #pragma unroll
             for (int i = 0; i < NI; ++i)
-                if (b * teams < have && in[i]) {
-                    const int64_t at = base + (off[b][i] + m * a.C);
-                    float d[V];
-                    for (int k = 0; k < V; ++k)
-                        d[k] = r[b] * (g[b][m][i][k] - (l == 0 ? s1[b] : 0.f) - x[b][m][i][k] * s2[b]);
-                    if (a.skip) {
-                        float e[V];
-                        load_vec<kF32, V>(a.skip, at, e);
-                        for (int k = 0; k < V; ++k) d[k] += e[k];
+                if (b < u.have && in[i])
+#pragma unroll
+                    for (int m = 0; m < R; ++m) {
+                        float o[V];
+                        for (int k = 0; k < V; ++k)
+                            o[k] = fmaf(-x[b][m][i][k], m2, l == 0 ? fmaf(r[b], g[b][m][i][k], -m1) : r[b] * g[b][m][i][k]);
+                        if (a.skip) {
+                            const float4 e = *reinterpret_cast<const float4*>(
+                                st + sl.o2 + ((team0 + b * R + m) * C + c[i]) * 4);
+                            o[0] += e.x; o[1] += e.y; o[2] += e.z; o[3] += e.w;
+                        }
+                        store_vec<kF32, V>(a.gx, base + ((b * teams * K + m) * C + c[i]), o);
                     }
-                    store_vec<kF32, V>(a.gx, at, d);
-                }
-    }
-}
-
-// Persistent blocks: block b takes chunks b, b + grid, ..., its warps the units
-// of those chunks in turn. The weight gradient stays in shared memory, one
-// private slot per lane, degree and channel, until the block's end: no atomics,
-// one fixed order.
-template <int XT, int NI>
-__global__ void __launch_bounds__(256, NI == 1 ? 2 : 1) k_norm_bwd_teams(NormBwdArgs a, int TL, int S, Units un,
-                                                                         int64_t chunks) {
-    extern __shared__ float4 acc4[];  // [8 warps][L + 2][NI][32 lanes]
-    const int teams = 32 / TL, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int per_warp = (a.L + 2) * NI * 32;
-    float4* acc = acc4 + warp * per_warp + lane;
-    for (int k = 0; k < (a.L + 2) * NI; ++k) acc[k * 32] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int64_t mine = (chunks - blockIdx.x + gridDim.x - 1) / gridDim.x * un.total;  // units of this block
-    for (int64_t k = warp; k < mine; k += 8) {
-        const int64_t c0 = (blockIdx.x + k / un.total * gridDim.x) * S, end = min(c0 + S, a.n);
-        int j = (int)(k % un.total), l = kMaxL;
-        while (j >= un.n[l]) j -= un.n[l--];
-        j *= teams;
-        switch (l) {
-            case 0: norm_bwd_unit<XT, NI, 0>(a, c0 + j * nodes_of(0, bwd_rows(NI)), end, TL, acc); break;
-            case 1: norm_bwd_unit<XT, NI, 1>(a, c0 + j * nodes_of(1, bwd_rows(NI)), end, TL, acc); break;
-            case 2: norm_bwd_unit<XT, NI, 2>(a, c0 + j * nodes_of(2, bwd_rows(NI)), end, TL, acc); break;
-            case 3: norm_bwd_unit<XT, NI, 3>(a, c0 + j * nodes_of(3, bwd_rows(NI)), end, TL, acc); break;
-            default: norm_bwd_unit<XT, NI, 4>(a, c0 + j * nodes_of(4, bwd_rows(NI)), end, TL, acc); break;
         }
     }
     if (!a.part) return;
-    __syncthreads();
-    // the block's sums over its warps and their teams, in order
-    const float* f = reinterpret_cast<const float*>(acc4);
-    for (int o = threadIdx.x; o < (a.L + 2) * a.C; o += 256) {
-        const int l = o / a.C, c = o % a.C, v = c / 4, i = v / TL, t = v % TL;
-        float s = 0.f;
-        for (int w = 0; w < 8; ++w)
-            for (int q = 0; q < teams; ++q) s += f[(w * per_warp + (l * NI + i) * 32 + q * TL + t) * 4 + c % 4];
-        a.part[(int64_t)blockIdx.x * (a.L + 2) * a.C + o] = s;
+    float* sh = reinterpret_cast<float*>(smem);  // the stages, free now: [warps][32 lanes][NI][V]
+#pragma unroll
+    for (int pass = 0; pass < (l == 0 ? 2 : 1); ++pass) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            for (int k = 0; k < V; ++k) sh[((warp * 32 + lane) * NI + i) * V + k] = pass == 0 ? dw[i][k] : db[i][k];
+        __syncthreads();
+        float* out = a.part + (int64_t)(blockIdx.x + (pass == 0 ? 0 : sl.at[kMaxL + 1])) * C;
+        for (int o = threadIdx.x; o < C; o += blockDim.x) {
+            const int vec = o / V, i = vec / TL, tt = vec % TL;
+            float sum = 0.f;
+            for (int q = 0; q < warps * teams; ++q) sum += sh[((q * TL + tt) * NI + i) * V + o % V];
+            out[o] = sum;
+        }
     }
+}
+
+template <int XT, int NI>
+__global__ void __launch_bounds__(32 * kBwdWarps, 2) k_norm_bwd_teams(NormBwdArgs a, int TL, Slots sl) {
+    extern __shared__ __align__(16) char smem[];
+    if (threadIdx.x < 16)
+        reinterpret_cast<float*>(smem + (blockDim.x >> 5) * sl.stages * sl.stage_bytes)[threadIdx.x] = 0.f;
+    __syncthreads();
+    const int blk = blockIdx.x;
+    if (blk < sl.at[1]) norm_bwd_degree<XT, NI, 0>(a, TL, sl, smem);
+    else if (blk < sl.at[2]) norm_bwd_degree<XT, NI, 1>(a, TL, sl, smem);
+    else if (blk < sl.at[3]) norm_bwd_degree<XT, NI, 2>(a, TL, sl, smem);
+    else if (blk < sl.at[4]) norm_bwd_degree<XT, NI, 3>(a, TL, sl, smem);
+    else norm_bwd_degree<XT, NI, 4>(a, TL, sl, smem);
 }
 
 // One block per (node, degree), the blocks split over the degrees as the rows
@@ -250,39 +263,39 @@ cudaError_t launch_bwd_rows(const NormBwdArgs& a, cudaStream_t s) {
 }
 
 template <int XT, int NI>
-cudaError_t launch_bwd_teams(const NormBwdArgs& a, const TeamPlan& p, int blocks, cudaStream_t s) {
-    const size_t smem = 8 * (size_t)(a.L + 2) * NI * 32 * sizeof(float4);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(k_norm_bwd_teams<XT, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
-        if (e != cudaSuccess) return e;
-    }
-    k_norm_bwd_teams<XT, NI><<<blocks, 256, smem, s>>>(a, p.TL, p.S, p.un, p.chunks);
+cudaError_t launch_bwd_teams(const NormBwdArgs& a, const TeamPlan& p, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(k_norm_bwd_teams<XT, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kBlockSmem);
+    if (e != cudaSuccess) return e;
+    const int row = kUnitRows * NI * 32, o1 = row * vec_bytes<XT>(), o2 = o1 + row * 16;
+    Slots sl{p.stage_bytes, p.stages, o1, o2, o2 + (a.skip ? row * 16 : 0), {}};
+    std::copy(p.at, p.at + kMaxL + 2, sl.at);
+    k_norm_bwd_teams<XT, NI><<<p.at[kMaxL + 1], 32 * p.warps, p.smem, s>>>(a, p.TL, sl);
     return cudaGetLastError();
 }
 
-// blocks of a backward call: rows of partials (teams), or blocks per row of features
-int bwd_blocks(int64_t n, int L, int C) {
-    if (use_teams(C)) return (int)std::min<int64_t>(team_plan(n, L, C, kBwdBlocks, false).chunks, kBwdBlocks);
+// blocks per row of features of k_norm_bwd_rows
+int rows_blocks(int64_t n, int L) {
     return (int)std::max<int64_t>(1, std::min<int64_t>(n, kNormBlocks / ((L + 1) * (L + 1))));
 }
 
 template <int XT>
 cudaError_t launch_bwd(NormBwdArgs a, float* gw, float* gb, cudaStream_t s) {
-    const int K = (a.L + 1) * (a.L + 1), blocks = bwd_blocks(a.n, a.L, a.C);
+    const int K = (a.L + 1) * (a.L + 1);
     JoinPlan j{};
     cudaError_t e;
     count_launch();
     if (use_teams(a.C)) {
-        const TeamPlan p = team_plan(a.n, a.L, a.C, kBwdBlocks, false);
-        e = p.NI == 1 ? launch_bwd_teams<XT, 1>(a, p, blocks, s) : launch_bwd_teams<XT, 2>(a, p, blocks, s);
-        j.stride = (int64_t)(a.L + 2) * a.C;
+        const TeamPlan p = team_plan(a.n, a.L, a.C, vec_bytes<XT>() + (a.skip ? 32 : 16), vec_bytes<XT>() + 32,
+                                     kStatBytes, kBwdWarps);
+        e = p.NI == 1 ? launch_bwd_teams<XT, 1>(a, p, s) : launch_bwd_teams<XT, 2>(a, p, s);
+        j.stride = a.C;
         for (int l = 0; l < a.L + 2; ++l) {
-            j.base[l] = (int64_t)l * a.C;
-            j.count[l] = blocks;
+            j.base[l] = (int64_t)(l <= a.L ? p.at[l] : p.at[kMaxL + 1]) * a.C;
+            j.count[l] = l <= a.L ? p.at[l + 1] - p.at[l] : p.at[1];
         }
     } else {
-        a.g = blocks;
+        a.g = rows_blocks(a.n, a.L);
         e = a.C % 4 == 0 ? launch_bwd_rows<XT, 4>(a, s) : launch_bwd_rows<XT, 1>(a, s);
         j.stride = a.C;
         for (int l = 0; l < a.L + 2; ++l) {
@@ -304,8 +317,8 @@ using namespace e2f;
 extern "C" size_t e2f_layer_norm_backward_workspace_size(int64_t n_atoms, const e2f_norm_cfg* cfg) {
     if (check_norm_cfg(cfg) != E2F_OK || n_atoms < 0) return 0;
     if (n_atoms == 0) return 256;
-    const int rows = use_teams(cfg->C) ? cfg->L + 2 : (cfg->L + 1) * (cfg->L + 1) + 1;
-    return align_up(4 * (size_t)bwd_blocks(n_atoms, cfg->L, cfg->C) * rows * cfg->C, 256);
+    if (use_teams(cfg->C)) return align_up(4 * (size_t)(2 * (kTeamBlocks + kMaxL)) * cfg->C, 256);
+    return align_up(4 * (size_t)rows_blocks(n_atoms, cfg->L) * ((cfg->L + 1) * (cfg->L + 1) + 1) * cfg->C, 256);
 }
 
 extern "C" e2f_status e2f_layer_norm_backward(const e2f_norm_cfg* cfg, int64_t n_atoms, const void* x,
@@ -330,7 +343,7 @@ extern "C" e2f_status e2f_layer_norm_backward(const e2f_norm_cfg* cfg, int64_t n
         reinterpret_cast<uintptr_t>(workspace) % 256)
         return E2F_ERR_ALIGNMENT;
     if (ws_bytes < e2f_layer_norm_backward_workspace_size(n_atoms, cfg)) return E2F_ERR_INVALID_ARG;
-    NormBwdArgs a{n_atoms, cfg->L, cfg->C, ck_blocks(cfg->C), x, x_scales, weight, mean, rstd, grad_y, grad_skip,
+    NormBwdArgs a{n_atoms, cfg->L, cfg->C, ck_blocks(cfg->C), 1.f / cfg->C, x, x_scales, weight, mean, rstd, grad_y, grad_skip,
                   grad_x, grad_weight || grad_bias ? static_cast<float*>(workspace) : nullptr, 0};
     E2F_CUDA_TRY(coded                       ? launch_bwd<kMXI8>(a, grad_weight, grad_bias, s)
                  : cfg->x_dtype == E2F_BF16 ? launch_bwd<kBF16>(a, grad_weight, grad_bias, s)
