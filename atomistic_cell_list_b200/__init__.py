@@ -460,36 +460,39 @@ def _operand(name: str, t: torch.Tensor, dtype: torch.dtype, shape, device=None)
     return t.data_ptr()
 
 
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """New memory for a call on `stream` (None: the current one), from that stream's pool."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)  # half the time of torch.empty
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _on(stream) -> int:
     """Handle of the stream of a call (None: the current one); it must belong to the current device."""
-    if stream is not None and stream.device_index != torch.cuda.current_device():
+    device = torch.cuda.current_device()
+    if stream is None:  # the handle alone: current_stream() builds an object, 3 us
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
         raise ValueError("stream must belong to the current CUDA device")
-    return _stream(stream)
+    return int(stream.cuda_stream)
 
 
-def _result(out: dict, name: str, dtype: torch.dtype, shape, device, stream) -> int:
+def _result(out: dict, name: str, dtype: torch.dtype, shape, like: torch.Tensor, stream) -> int:
     """Address of out[name], allocated here when the caller did not give it."""
     t = out.get(name)
     if t is None:
-        t = out[name] = _empty(shape, dtype, device, stream)
+        t = out[name] = _empty(shape, dtype, like, stream)
         return t.data_ptr()
-    return _operand(f"out[{name!r}]", t, dtype, shape, device)
+    return _operand(f"out[{name!r}]", t, dtype, shape, like.device)
 
 
-def _scratch(workspace, n_bytes: int, device, stream) -> torch.Tensor:
+def _scratch(workspace, n_bytes: int, like: torch.Tensor, stream) -> torch.Tensor:
     """The caller's workspace, or a new one when it is absent or too small."""
     if workspace is None or workspace.numel() < n_bytes:
-        return _empty(max(n_bytes, 256), torch.uint8, device, stream)
-    if workspace.dtype is not torch.uint8 or workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+        return _empty((max(n_bytes, 256),), torch.uint8, like, stream)
+    if workspace.dtype is not torch.uint8 or workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
     return workspace
 
 
@@ -505,7 +508,7 @@ def e2f_layer_norm(cfg: e2f_norm_cfg, x, weight, bias=None, residual=None, x_sca
     under these names are written in place of new ones; out["sum"] may be x."""
     L, C = cfg.L, cfg.C
     K, n = (L + 1) ** 2, x.shape[0] if x.dim() else 0
-    shape, dev = torch.Size((n, K, C)), x.device
+    shape, dev = (n, K, C), x.device
     xt = _TORCH[cfg.x_dtype]
     px = _operand("x", x, xt, shape)
     pw = _operand("weight", weight, torch.float32, (L + 1, C), dev)
@@ -519,14 +522,14 @@ def e2f_layer_norm(cfg: e2f_norm_cfg, x, weight, bias=None, residual=None, x_sca
         ps = _operand("x_scales", x_scales, torch.uint8, (n, K, nb), dev)
     if residual is not None:
         pr = _operand("residual", residual, torch.float32, shape, dev)
-        psum = _result(res, "sum", xt, shape, dev, stream)
-    py = _result(res, "y", _TORCH[cfg.y_dtype], shape, dev, stream)
+        psum = _result(res, "sum", xt, shape, x, stream)
+    py = _result(res, "y", _TORCH[cfg.y_dtype], shape, x, stream)
     if stats:
-        pm = _result(res, "mean", torch.float32, (n,), dev, stream)
-        pi = _result(res, "rstd", torch.float32, (n, L + 1), dev, stream)
+        pm = _result(res, "mean", torch.float32, (n,), x, stream)
+        pi = _result(res, "rstd", torch.float32, (n, L + 1), x, stream)
     if checkpoint:
-        pc = _result(res, "codes", torch.int8, shape, dev, stream)
-        pcs = _result(res, "scales", torch.uint8, (n, K, nb), dev, stream)
+        pc = _result(res, "codes", torch.int8, shape, x, stream)
+        pcs = _result(res, "scales", torch.uint8, (n, K, nb), x, stream)
     _check(lib().e2f_layer_norm(ctypes.byref(cfg), n, px, ps, pr, pw, pb, psum, py, pm, pi, pc, pcs, _on(stream)),
            "e2f_layer_norm")
     return res
@@ -543,7 +546,7 @@ def e2f_layer_norm_backward(cfg: e2f_norm_cfg, x, weight, mean, rstd, grad_y, gr
     (all fp32). out["x"] may be grad_skip or grad_y."""
     L, C = cfg.L, cfg.C
     K, n = (L + 1) ** 2, x.shape[0] if x.dim() else 0
-    shape, dev, f32 = torch.Size((n, K, C)), x.device, torch.float32
+    shape, dev, f32 = (n, K, C), x.device, torch.float32
     px = _operand("x", x, _TORCH[cfg.x_dtype], shape)
     ps = None
     if cfg.x_dtype == E2F_MXI8:
@@ -556,12 +559,12 @@ def e2f_layer_norm_backward(cfg: e2f_norm_cfg, x, weight, mean, rstd, grad_y, gr
     pg = _operand("grad_y", grad_y, f32, shape, dev)
     pk = None if grad_skip is None else _operand("grad_skip", grad_skip, f32, shape, dev)
     g = {} if out is None else dict(out)
-    pgx = _result(g, "x", f32, shape, dev, stream)
+    pgx = _result(g, "x", f32, shape, x, stream)
     pgw = pgb = None
     if want_weights:
-        pgw = _result(g, "weight", f32, (L + 1, C), dev, stream)
-        pgb = _result(g, "bias", f32, (C,), dev, stream)
-    workspace = _scratch(workspace, e2f_layer_norm_backward_workspace_size(n, cfg), dev, stream)
+        pgw = _result(g, "weight", f32, (L + 1, C), x, stream)
+        pgb = _result(g, "bias", f32, (C,), x, stream)
+    workspace = _scratch(workspace, e2f_layer_norm_backward_workspace_size(n, cfg), x, stream)
     _check(lib().e2f_layer_norm_backward(ctypes.byref(cfg), n, px, ps, pw, pm, pi, pg, pk, pgx, pgw, pgb,
                                          workspace.data_ptr(), workspace.numel(), _on(stream)),
            "e2f_layer_norm_backward")
@@ -575,8 +578,8 @@ def e2f_checkpoint_store(x: torch.Tensor, out: dict | None = None, stream=None):
         raise ValueError("x must be an fp32 or bf16 tensor of at least one dimension")
     px, C = _operand("x", x, x.dtype, x.shape), x.shape[-1]
     res = {} if out is None else dict(out)
-    pc = _result(res, "codes", torch.int8, x.shape, x.device, stream)
-    ps = _result(res, "scales", torch.uint8, x.shape[:-1] + ((C + 31) // 32,), x.device, stream)
+    pc = _result(res, "codes", torch.int8, x.shape, x, stream)
+    ps = _result(res, "scales", torch.uint8, x.shape[:-1] + ((C + 31) // 32,), x, stream)
     _check(lib().e2f_checkpoint_store(px, E2F_F32 if x.dtype is torch.float32 else E2F_BF16,
                                       x.numel() // max(C, 1), C, pc, ps, _on(stream)), "e2f_checkpoint_store")
     return res["codes"], res["scales"]
@@ -590,7 +593,7 @@ def e2f_checkpoint_load(codes: torch.Tensor, scales: torch.Tensor, dtype: str = 
     pc, C = _operand("codes", codes, torch.int8, codes.shape), codes.shape[-1]
     ps = _operand("scales", scales, torch.uint8, codes.shape[:-1] + ((C + 31) // 32,), codes.device)
     res = {} if out is None else {"out": out}
-    po = _result(res, "out", _TORCH[_DTYPES[dtype]], codes.shape, codes.device, stream)
+    po = _result(res, "out", _TORCH[_DTYPES[dtype]], codes.shape, codes, stream)
     _check(lib().e2f_checkpoint_load(pc, ps, codes.numel() // max(C, 1), C, _DTYPES[dtype], po, _on(stream)),
            "e2f_checkpoint_load")
     return res["out"]
@@ -609,8 +612,8 @@ def e2f_embedding(cfg: e2f_embed_cfg, tokens, table, out: torch.Tensor | None = 
     pt = _operand("tokens", tokens, torch.int32, (n,))
     pw = _operand("table", table, _TORCH[cfg.table_dtype], (cfg.n_tokens, cfg.C), dev)
     res = {} if out is None else {"out": out}
-    po = _result(res, "out", _TORCH[cfg.out_dtype], (n, (cfg.L + 1) ** 2, cfg.C), dev, stream)
-    ws = _empty(256, torch.uint8, dev, stream) if check else None
+    po = _result(res, "out", _TORCH[cfg.out_dtype], (n, (cfg.L + 1) ** 2, cfg.C), tokens, stream)
+    ws = _empty((256,), torch.uint8, tokens, stream) if check else None
     s = _on(stream)
     _check(lib().e2f_embedding(ctypes.byref(cfg), pt, n, pw, po, _ptr(ws), 256 if check else 0, s), "e2f_embedding")
     if check:
@@ -629,8 +632,8 @@ def e2f_embedding_backward(cfg: e2f_embed_cfg, tokens, grad_out, workspace: torc
     pt = _operand("tokens", tokens, torch.int32, (n,))
     pg = _operand("grad_out", grad_out, torch.float32, (n, (cfg.L + 1) ** 2, cfg.C), dev)
     res = {} if out is None else {"out": out}
-    po = _result(res, "out", torch.float32, (cfg.n_tokens, cfg.C), dev, stream)
-    workspace = _scratch(workspace, e2f_embedding_backward_workspace_size(n, cfg), dev, stream)
+    po = _result(res, "out", torch.float32, (cfg.n_tokens, cfg.C), tokens, stream)
+    workspace = _scratch(workspace, e2f_embedding_backward_workspace_size(n, cfg), tokens, stream)
     s = _on(stream)
     _check(lib().e2f_embedding_backward(ctypes.byref(cfg), pt, n, pg, po, _ptr(workspace), workspace.numel(), s),
            "e2f_embedding_backward")

@@ -1,9 +1,13 @@
 // Species embedding: out[n,0,:] = scale table[token_n,:] (higher degrees zero),
 // and its gradient, grad_table[v,:] = scale sum_{n: token_n = v} grad_out[n,0,:].
 //
-// The gradient sorts the tokens (a stable radix sort, 8 bits a pass, so equal
-// tokens keep their order) and sums runs of equal tokens over fixed chunks of
-// the sorted order; a run that crosses chunks is joined from its chunks' sums.
+// The gradient sums runs of equal tokens in sorted order. A block takes a tile of
+// T tokens; teams of lanes sum equal parts of the tile, run by run; the runs that
+// cross parts are added in the block, those that cross tiles by a second kernel.
+//   Tables of up to 256 rows (species): each tile is sorted by itself, in shared
+//   memory. A block's sums of its distinct tokens are at most half of what it
+//   reads, and two launches do it all (one for a single tile).
+//   Larger tables: a stable radix sort of all tokens first, 8 bits a pass.
 // Every sum has one fixed order and no atomics, so results repeat bit for bit.
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -19,30 +23,44 @@ namespace {
 
 constexpr int kMaxEmbedC = 16384;
 constexpr int kSortTile = 1024;  // tokens of a sorting block (256 threads, 4 each)
-constexpr int kRunChunk = 64;    // sorted tokens summed by one team of lanes
+constexpr int kLocalTokens = 256;  // largest table whose tiles are sorted one by one
+constexpr int kMaxTile = 2048;
 
 struct EmbedWs {
     size_t o_status, o_hist, o_tot, o_key[2], o_idx[2], o_part, bytes;
-    int64_t tiles, chunks;
-    int passes;
+    int64_t sort_tiles, tiles;
+    int tile, passes, V, TL;
 };
 
 EmbedWs embed_layout(int64_t n, const e2f_embed_cfg& c) {
     EmbedWs w{};
     size_t o = 0;
     auto take = [&](size_t b) { size_t r = o; o = align_up(o + b, 256); return r; };
-    w.passes = 1;
-    while (w.passes < 4 && ((int64_t)c.n_tokens >> (8 * w.passes))) ++w.passes;
-    w.tiles = (n + kSortTile - 1) / kSortTile;
-    w.chunks = (n + kRunChunk - 1) / kRunChunk;
+    w.V = c.C % 4 == 0 ? 4 : 1;
+    w.TL = 1;
+    while (w.TL < 32 && w.TL * w.V < c.C) w.TL *= 2;
+    // up to two tiles per SM, 8 tokens a team at least; what one block sorts fast goes to one block
+    const bool local = c.n_tokens <= kLocalTokens;
+    w.tile = std::max(64, 8 * (256 / w.TL));
+    while (w.tile < kMaxTile && (n + w.tile - 1) / w.tile > 296) w.tile *= 2;
+    if (local && n <= 512) w.tile = std::max(w.tile, 512);
+    w.tiles = (n + w.tile - 1) / w.tile;
     w.o_status = take(256);  // first: e2f_attention_status reads it
-    w.o_hist = take(4 * 256 * (size_t)w.tiles);
-    w.o_tot = take(4 * 256);
-    for (int k = 0; k < 2; ++k) {
-        w.o_key[k] = take(4 * (size_t)n);
-        w.o_idx[k] = take(4 * (size_t)n);
+    if (local) {
+        w.o_hist = take((size_t)w.tiles * c.n_tokens);  // which tokens a tile has
+        w.o_part = take(w.tiles > 1 ? 4 * (size_t)w.tiles * c.n_tokens * c.C : 0);
+    } else {
+        w.passes = 1;
+        while (w.passes < 4 && ((int64_t)c.n_tokens >> (8 * w.passes))) ++w.passes;
+        w.sort_tiles = (n + kSortTile - 1) / kSortTile;
+        w.o_hist = take(4 * 256 * (size_t)w.sort_tiles);
+        w.o_tot = take(4 * 256);
+        for (int k = 0; k < 2; ++k) {
+            w.o_key[k] = take(4 * (size_t)n);
+            w.o_idx[k] = take(4 * (size_t)n);
+        }
+        w.o_part = take(8 * (size_t)w.tiles * c.C);
     }
-    w.o_part = take(8 * (size_t)w.chunks * c.C);
     w.bytes = o;
     return w;
 }
@@ -182,72 +200,252 @@ __global__ void __launch_bounds__(256) k_sort_place(const void* keys, const int*
     }
 }
 
-// A team of lanes sums one chunk of the sorted tokens, run by run. A run that
-// begins and ends in the chunk is final; one that begins here and goes on is
-// the chunk's open sum (part[2 chunk + 1]); one that came in from the chunk
-// before is its carry (part[2 chunk]).
-template <int V>
-__global__ void __launch_bounds__(256) k_run_sum(const float* g, int64_t row_stride, int C, const uint32_t* keys,
-                                                 const int* idx, int64_t n, uint32_t n_tokens, float scale, int team,
-                                                 float* grad, float* part) {
-    const int64_t chunk = (blockIdx.x * 256ll + threadIdx.x) / team;
-    const int c = (blockIdx.y * team + threadIdx.x % team) * V;
-    const int64_t p0 = chunk * kRunChunk, p1 = min(p0 + kRunChunk, n);
-    if (p0 >= n || c >= C) return;
-    float acc[V] = {};
-    uint32_t cur = keys[p0];
-    bool begins = p0 == 0 || keys[p0 - 1] != cur;
-    auto flush = [&](bool ends) {
-        if (cur >= n_tokens) return;
-        float v[V];
-        for (int k = 0; k < V; ++k) v[k] = acc[k] * (begins && ends ? scale : 1.f);
-        if (begins && ends) store_vec<kF32, V>(grad, (int64_t)cur * C + c, v);
-        else store_vec<kF32, V>(part, (2 * chunk + (begins ? 1 : 0)) * C + c, v);
-    };
-    constexpr int U = 8;
-    for (int64_t p = p0; p < p1; p += U) {
-        uint32_t key[U];
-        float v[U][V];
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            key[j] = p + j < p1 ? keys[p + j] : n_tokens;
-            for (int k = 0; k < V; ++k) v[j][k] = 0.f;
-            if (p + j < p1 && key[j] < n_tokens) load_vec<kF32, V>(g, idx[p + j] * row_stride + c, v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (p + j >= p1) break;
-            if (key[j] != cur) {
-                flush(true);
-                cur = key[j];
-                begins = true;
-                for (int k = 0; k < V; ++k) acc[k] = 0.f;
+// Sorts the tile's tokens in shared memory, equal ones in their order; cnt holds
+// how often each occurs. 256 threads; a warp takes a contiguous part of the tile.
+__device__ __forceinline__ void sort_tile(const int32_t* tok, int64_t base, int n, int tile, int n_tokens,
+                                          uint32_t* keys, int* idx, uint32_t (*wc)[257], uint32_t* cnt, int* status) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, part = tile / 8;
+    for (int k = threadIdx.x; k < 8 * 257; k += 256) wc[0][k] = 0;
+    __syncthreads();
+    // two sweeps over the warp's part: counts, then places (the second repeats the ranks)
+    for (int sweep = 0; sweep < 2; ++sweep) {
+        for (int j = 0; j < part; j += 32) {
+            const int p = w * part + j + lane;
+            const bool ok = j + lane < part && p < n;
+            uint32_t key = 0;
+            if (ok) {
+                const int t = tok[base + p];
+                if (sweep == 0 && t >= n_tokens && status) *status = E2F_ERR_INVALID_ARG;
+                key = sort_key(t, n_tokens);
             }
-            for (int k = 0; k < V; ++k) acc[k] += v[j][k];
+            const uint32_t same = __match_any_sync(0xffffffffu, ok ? key : 0xffffffffu);
+            const uint32_t below = __popc(same & ((1u << lane) - 1u));
+            const uint32_t at = ok ? wc[w][key] + below : 0u;
+            __syncwarp();
+            if (ok && below == 0) wc[w][key] += __popc(same);
+            __syncwarp();
+            if (sweep == 1 && ok) {
+                keys[at] = key;
+                idx[at] = (int)(base + p);
+            }
+        }
+        __syncthreads();
+        if (sweep == 0) {
+            // token k's places: smaller tokens, then the warps before (thread k, and the last key by thread 0)
+            __shared__ uint32_t ws[8];
+            uint32_t all = 0;
+            for (int q = 0; q < 8; ++q) all += wc[q][threadIdx.x];
+            cnt[threadIdx.x] = all;
+            uint32_t inc = all;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            if (lane == 31) ws[w] = inc;
+            __syncthreads();
+            uint32_t at = inc - all;
+            for (int q = 0; q < w; ++q) at += ws[q];
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t c = wc[q][threadIdx.x];
+                wc[q][threadIdx.x] = at;
+                at += c;
+            }
+            __syncthreads();
+            if (threadIdx.x == 255)  // key 256: padding of a table of 256 rows
+                for (int q = 0; q < 8; ++q) {
+                    const uint32_t c = wc[q][256];
+                    wc[q][256] = at;
+                    at += c;
+                }
+            __syncthreads();
         }
     }
-    flush(p1 == n || keys[p1] != cur);
 }
 
-// Block (chunk, 32 columns): if a run opened in the chunk, adds the carries of the chunks it reaches.
-__global__ void __launch_bounds__(1024) k_run_join(const float* part, int C, const uint32_t* keys, int64_t n,
-                                                   uint32_t n_tokens, int64_t chunks, float scale, float* grad) {
-    __shared__ float sh[32][33];
-    const int64_t s = blockIdx.x, p0 = s * kRunChunk, p1 = p0 + kRunChunk;
-    if (p1 >= n) return;
-    const uint32_t key = keys[p1 - 1];
-    if (key >= n_tokens || keys[p1] != key) return;              // nothing goes on
-    if (p0 > 0 && keys[p0] == key && keys[p0 - 1] == key) return;  // it did not begin here
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.y * 32 + lane;
-    float sum = w == 0 && c < C ? part[(2 * s + 1) * C + c] : 0.f;
-    for (int64_t j = s + 1 + w; j < chunks && keys[j * kRunChunk] == key; j += 32)
-        if (c < C) sum += part[2 * j * C + c];
-    sh[w][lane] = sum;
-    __syncthreads();
-    if (w == 0 && c < C) {
-        for (int k = 1; k < 32; ++k) sum += sh[k][lane];
-        grad[(int64_t)key * C + c] = scale * sum;
+struct RunArgs {
+    const float* g;
+    int64_t row_stride, n;
+    int C, n_tokens, tile, TL;
+    float scale;
+    float* grad;
+    float* part;
+    // tables of up to 256 rows
+    const int32_t* tok;
+    uint8_t* has;
+    int* status;
+    // larger tables: all tokens sorted
+    const uint32_t* keys;
+    const int* idx;
+};
+
+// One tile, TL V columns. LOCAL: sorts the tile and writes its sums by token to
+// part[tile][token] (to the table itself when there is one tile). Otherwise runs
+// inside the tile are final; one that begins here and goes on is the tile's open
+// sum (part[2 tile + 1]), one that came in from the tile before its carry
+// (part[2 tile]).
+template <int V, bool LOCAL>
+__global__ void __launch_bounds__(256) k_run_sum(RunArgs a) {
+    extern __shared__ uint32_t sm[];  // [tile] keys, [tile] indexes, then LOCAL: [8][257] counts, [256] totals
+    __shared__ __align__(16) float ent[256 * 2 * V];  // [team][first, last run][TL V]
+    __shared__ uint32_t ent_key[256][2];
+    uint32_t* keys = sm;
+    int* idx = reinterpret_cast<int*>(sm + a.tile);
+    const int64_t base = (int64_t)blockIdx.x * a.tile;
+    const int n = (int)min((int64_t)a.tile, a.n - base);
+    const uint32_t none = 0xffffffffu, n_tokens = (uint32_t)a.n_tokens;
+    if constexpr (LOCAL) {
+        uint32_t (*wc)[257] = reinterpret_cast<uint32_t (*)[257]>(sm + 2 * a.tile);
+        uint32_t* cnt = sm + 2 * a.tile + 8 * 257;
+        sort_tile(a.tok, base, n, a.tile, a.n_tokens, keys, idx, wc, cnt, a.status);
+        const int k = threadIdx.x;
+        if (gridDim.x > 1) {
+            if (k < a.n_tokens) a.has[(int64_t)blockIdx.x * a.n_tokens + k] = cnt[k] != 0;
+        }
+    } else {
+        for (int p = threadIdx.x; p < n; p += 256) {
+            keys[p] = a.keys[base + p];
+            idx[p] = a.idx[base + p];
+        }
+        __syncthreads();
     }
+    const int team = threadIdx.x / a.TL, teams = 256 / a.TL, t = threadIdx.x % a.TL;
+    const int c = (blockIdx.y * a.TL + t) * V, per = a.tile / teams;
+    const bool in = c < a.C;
+    const int p0 = min(team * per, n), p1 = min(p0 + per, n);
+    float* row_out = LOCAL ? (gridDim.x > 1 ? a.part + (int64_t)blockIdx.x * a.n_tokens * a.C : a.grad) : a.grad;
+    const float f = LOCAL && gridDim.x > 1 ? 1.f : a.scale;
+    auto final_row = [&](uint32_t key, const float (&v)[V]) {
+        if (key >= n_tokens || !in) return;
+        float o[V];
+        for (int k = 0; k < V; ++k) o[k] = v[k] * f;
+        store_vec<kF32, V>(row_out, (int64_t)key * a.C + c, o);
+    };
+    // this team's part
+    {
+        uint32_t cur = p0 < p1 ? keys[p0] : none;
+        bool first = true;
+        float acc[V] = {};
+        constexpr int U = 8;
+        for (int p = p0; p < p1; p += U) {
+            uint32_t key[U];
+            float v[U][V];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                key[j] = p + j < p1 ? keys[p + j] : n_tokens;
+                for (int k = 0; k < V; ++k) v[j][k] = 0.f;
+                if (key[j] < n_tokens && in) load_vec<kF32, V>(a.g, idx[p + j] * a.row_stride + c, v[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (p + j >= p1) break;
+                if (key[j] != cur) {
+                    if (first) {
+                        for (int k = 0; k < V; ++k) ent[(team * 2 * a.TL + t) * V + k] = acc[k];
+                        if (t == 0) ent_key[team][0] = cur;
+                        first = false;
+                    } else {
+                        final_row(cur, acc);
+                    }
+                    cur = key[j];
+                    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+                }
+                for (int k = 0; k < V; ++k) acc[k] += v[j][k];
+            }
+        }
+        const int e = first ? 0 : 1;
+        for (int k = 0; k < V; ++k) ent[((team * 2 + e) * a.TL + t) * V + k] = acc[k];
+        if (t == 0) {
+            ent_key[team][e] = cur;
+            if (e == 0) ent_key[team][1] = none;
+        }
+    }
+    __syncthreads();
+    // the tile's first and last runs of all parts, in order
+    if (team == 0) {
+        bool begins = LOCAL || base == 0 || a.keys[base - 1] != keys[0];
+        uint32_t cur = keys[0];
+        float acc[V] = {};
+        auto flush = [&](bool ends) {
+            if (begins && ends) return final_row(cur, acc);
+            if (cur < n_tokens && in)
+                store_vec<kF32, V>(a.part, (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * a.C + c, acc);
+        };
+        for (int q = 0; q < 2 * teams; ++q) {
+            const uint32_t key = ent_key[q >> 1][q & 1];
+            if (key == none) continue;
+            if (key != cur) {
+                flush(true);
+                begins = true;
+                cur = key;
+                for (int k = 0; k < V; ++k) acc[k] = 0.f;
+            }
+            for (int k = 0; k < V; ++k) acc[k] += ent[(q * a.TL + t) * V + k];
+        }
+        flush(LOCAL || base + n == a.n || a.keys[base + n] != cur);
+    }
+    if constexpr (LOCAL)
+        if (gridDim.x == 1) {  // rows of tokens that do not occur
+            const uint32_t* cnt = sm + 2 * a.tile + 8 * 257;
+            const float zero[V] = {};
+            for (int k = team; k < a.n_tokens; k += teams)
+                if (cnt[k] == 0 && in) store_vec<kF32, V>(a.grad, (int64_t)k * a.C + c, zero);
+        }
+}
+
+constexpr int kJoinWarps = 16;
+
+// sum of the block's warps, in order, by its first warp; true there
+template <int V>
+__device__ __forceinline__ bool join_warps(float (&v)[V]) {
+    __shared__ float sh[kJoinWarps][32][V];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    for (int k = 0; k < V; ++k) sh[w][lane][k] = v[k];
+    __syncthreads();
+    if (w) return false;
+    for (int q = 1; q < kJoinWarps; ++q)
+        for (int k = 0; k < V; ++k) v[k] += sh[q][lane][k];
+    return true;
+}
+
+// Block (token, 32 V columns): adds the tiles' sums of the token.
+template <int V>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_token_join(RunArgs a, int64_t tiles) {
+    const int key = blockIdx.x, c = (blockIdx.y * 32 + (threadIdx.x & 31)) * V;
+    float acc[V] = {};
+    if (c < a.C)
+#pragma unroll 4
+        for (int64_t b = threadIdx.x >> 5; b < tiles; b += kJoinWarps)
+            if (a.has[b * a.n_tokens + key]) {
+                float v[V];
+                load_vec<kF32, V>(a.part, (b * a.n_tokens + key) * a.C + c, v);
+                for (int k = 0; k < V; ++k) acc[k] += v[k];
+            }
+    if (!join_warps<V>(acc) || c >= a.C) return;
+    for (int k = 0; k < V; ++k) acc[k] *= a.scale;
+    store_vec<kF32, V>(a.grad, (int64_t)key * a.C + c, acc);
+}
+
+// Block (tile, 32 V columns): if a run opened in the tile, adds the carries of the tiles it reaches.
+template <int V>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_run_join(RunArgs a, int64_t tiles) {
+    const int64_t s = blockIdx.x, p0 = s * a.tile, p1 = p0 + a.tile;
+    if (p1 >= a.n) return;
+    const uint32_t key = a.keys[p1 - 1];
+    if (key >= (uint32_t)a.n_tokens || a.keys[p1] != key) return;        // nothing goes on
+    if (p0 > 0 && a.keys[p0] == key && a.keys[p0 - 1] == key) return;  // it did not begin here
+    const int w = threadIdx.x >> 5, c = (blockIdx.y * 32 + (threadIdx.x & 31)) * V;
+    float acc[V] = {}, v[V];
+    if (c < a.C) {
+        if (w == 0) load_vec<kF32, V>(a.part, (2 * s + 1) * a.C + c, acc);
+#pragma unroll 4
+        for (int64_t j = s + 1 + w; j < tiles && a.keys[j * a.tile] == key; j += kJoinWarps) {
+            load_vec<kF32, V>(a.part, 2 * j * a.C + c, v);
+            for (int k = 0; k < V; ++k) acc[k] += v[k];
+        }
+    }
+    if (!join_warps<V>(acc) || c >= a.C) return;
+    for (int k = 0; k < V; ++k) acc[k] *= a.scale;
+    store_vec<kF32, V>(a.grad, (int64_t)key * a.C + c, acc);
 }
 
 template <int TT, int YT>
@@ -263,10 +461,26 @@ cudaError_t launch_embed(const e2f_embed_cfg& f, const int32_t* tok, int64_t n, 
     return cudaGetLastError();
 }
 
+template <int V>
 cudaError_t run_embed_bwd(const e2f_embed_cfg& f, const int32_t* tok, int64_t n, const float* g, float* grad, char* ws,
                           const EmbedWs& w, cudaStream_t s) {
     const int K = (f.L + 1) * (f.L + 1);
     int* status = reinterpret_cast<int*>(ws + w.o_status);
+    RunArgs a{g, (int64_t)K * f.C, n, f.C, f.n_tokens, w.tile, w.TL, f.scale, grad,
+              reinterpret_cast<float*>(ws + w.o_part)};
+    const dim3 grid((unsigned)w.tiles, (unsigned)((f.C + w.TL * V - 1) / (w.TL * V)));
+    if (f.n_tokens <= kLocalTokens) {
+        a.tok = tok;
+        a.has = reinterpret_cast<uint8_t*>(ws + w.o_hist);
+        a.status = status;
+        k_run_sum<V, true><<<grid, 256, 4 * (2 * w.tile + 8 * 257 + 256), s>>>(a);
+        count_launch();
+        if (w.tiles > 1) {
+            k_token_join<V><<<dim3(f.n_tokens, (f.C + 32 * V - 1) / (32 * V)), 32 * kJoinWarps, 0, s>>>(a, w.tiles);
+            count_launch();
+        }
+        return cudaGetLastError();
+    }
     uint32_t* hist = reinterpret_cast<uint32_t*>(ws + w.o_hist);
     uint32_t* total = reinterpret_cast<uint32_t*>(ws + w.o_tot);
     uint32_t* key[2];
@@ -275,40 +489,30 @@ cudaError_t run_embed_bwd(const e2f_embed_cfg& f, const int32_t* tok, int64_t n,
         key[k] = reinterpret_cast<uint32_t*>(ws + w.o_key[k]);
         idx[k] = reinterpret_cast<int*>(ws + w.o_idx[k]);
     }
-    float* part = reinterpret_cast<float*>(ws + w.o_part);
     cudaError_t e = cudaMemsetAsync(grad, 0, 4 * (size_t)f.n_tokens * f.C, s);
     if (e != cudaSuccess) return e;
-    const unsigned tiles = (unsigned)w.tiles;
+    const unsigned tiles = (unsigned)w.sort_tiles;
     for (int p = 0; p < w.passes; ++p) {
         const int to = p & 1, from = to ^ 1;
         if (p == 0) {
-            k_sort_count<true><<<tiles, 256, 0, s>>>(tok, n, f.n_tokens, 0, w.tiles, hist, status);
-            k_sort_scan<<<256, 256, 0, s>>>(hist, w.tiles, total);
-            k_sort_place<true><<<tiles, 256, 0, s>>>(tok, nullptr, n, f.n_tokens, 0, w.tiles, hist, total, key[to],
+            k_sort_count<true><<<tiles, 256, 0, s>>>(tok, n, f.n_tokens, 0, w.sort_tiles, hist, status);
+            k_sort_scan<<<256, 256, 0, s>>>(hist, w.sort_tiles, total);
+            k_sort_place<true><<<tiles, 256, 0, s>>>(tok, nullptr, n, f.n_tokens, 0, w.sort_tiles, hist, total, key[to],
                                                      idx[to]);
         } else {
-            k_sort_count<false><<<tiles, 256, 0, s>>>(key[from], n, f.n_tokens, 8 * p, w.tiles, hist, nullptr);
-            k_sort_scan<<<256, 256, 0, s>>>(hist, w.tiles, total);
-            k_sort_place<false><<<tiles, 256, 0, s>>>(key[from], idx[from], n, f.n_tokens, 8 * p, w.tiles, hist, total,
-                                                      key[to], idx[to]);
+            k_sort_count<false><<<tiles, 256, 0, s>>>(key[from], n, f.n_tokens, 8 * p, w.sort_tiles, hist, nullptr);
+            k_sort_scan<<<256, 256, 0, s>>>(hist, w.sort_tiles, total);
+            k_sort_place<false><<<tiles, 256, 0, s>>>(key[from], idx[from], n, f.n_tokens, 8 * p, w.sort_tiles, hist,
+                                                      total, key[to], idx[to]);
         }
         count_launch(3);
     }
-    const int at = (w.passes - 1) & 1;
-    const int V = f.C % 4 == 0 ? 4 : 1;
-    int team = 1;
-    while (team < 32 && team * V < f.C) team *= 2;
-    const dim3 grid((unsigned)((w.chunks * team + 255) / 256), (unsigned)((f.C + team * V - 1) / (team * V)));
-    if (V == 4)
-        k_run_sum<4><<<grid, 256, 0, s>>>(g, (int64_t)K * f.C, f.C, key[at], idx[at], n, (uint32_t)f.n_tokens, f.scale,
-                                          team, grad, part);
-    else
-        k_run_sum<1><<<grid, 256, 0, s>>>(g, (int64_t)K * f.C, f.C, key[at], idx[at], n, (uint32_t)f.n_tokens, f.scale,
-                                          team, grad, part);
+    a.keys = key[(w.passes - 1) & 1];
+    a.idx = idx[(w.passes - 1) & 1];
+    k_run_sum<V, false><<<grid, 256, 8 * w.tile, s>>>(a);
     count_launch();
-    if (w.chunks > 1) {
-        k_run_join<<<dim3((unsigned)w.chunks, (unsigned)((f.C + 31) / 32)), 1024, 0, s>>>(
-            part, f.C, key[at], n, (uint32_t)f.n_tokens, w.chunks, f.scale, grad);
+    if (w.tiles > 1) {
+        k_run_join<V><<<dim3((unsigned)w.tiles, (f.C + 32 * V - 1) / (32 * V)), 32 * kJoinWarps, 0, s>>>(a, w.tiles);
         count_launch();
     }
     return cudaGetLastError();
@@ -372,6 +576,8 @@ extern "C" e2f_status e2f_embedding_backward(const e2f_embed_cfg* cfg, const int
         E2F_CUDA_TRY(cudaMemsetAsync(grad_table, 0, 4 * (size_t)cfg->n_tokens * cfg->C, s));
         return E2F_OK;
     }
-    E2F_CUDA_TRY(run_embed_bwd(*cfg, tokens, n_atoms, grad_out, grad_table, static_cast<char*>(workspace), w, s));
+    char* ws = static_cast<char*>(workspace);
+    E2F_CUDA_TRY(w.V == 4 ? run_embed_bwd<4>(*cfg, tokens, n_atoms, grad_out, grad_table, ws, w, s)
+                          : run_embed_bwd<1>(*cfg, tokens, n_atoms, grad_out, grad_table, ws, w, s));
     return E2F_OK;
 }
