@@ -65,25 +65,45 @@ EmbedWs embed_layout(int64_t n, const e2f_embed_cfg& c) {
     return w;
 }
 
+// V = 1, 4 or 8 values from an index that is a multiple of V
+template <int T, int V>
+__device__ __forceinline__ void load_row(const void* p, int64_t i, float (&v)[V]) {
+    if constexpr (V == 8) load8<T>(p, i / 8, v);
+    else load_vec<T, V>(p, i, v);
+}
+template <int T, int V>
+__device__ __forceinline__ void store_row(void* p, int64_t i, const float (&v)[V]) {
+    if constexpr (V == 8) store8<T>(p, i / 8, v);
+    else store_vec<T, V>(p, i, v);
+}
+
+// 16 bytes of values: 8 of bf16, 4 of fp32
+template <int T>
+constexpr int kWide = T == kBF16 ? 8 : 4;
+
+// One group of `lanes` lanes (a power of two) per node: its first C values from
+// the table, zeros behind them. V values a store; the write of the output bounds it.
 template <int TT, int YT, int V>
 __global__ void __launch_bounds__(256) k_embed(const int32_t* tok, int64_t n, const void* table, int n_tokens, int K,
-                                               int C, float scale, void* out, int* status) {
-    const int cv = C / V;
-    const int64_t total = n * K * cv, step = (int64_t)gridDim.x * 256;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += step) {
-        const int64_t row = i / cv, node = row / K;
-        const int c = (int)(i - row * cv) * V;
-        float v[V] = {};
-        if (row == node * K) {
-            const int t = tok[node];
-            if (t >= 0 && t < n_tokens) {
-                load_vec<TT, V>(table, (int64_t)t * C + c, v);
+                                               int C, float scale, int lanes, void* out, int* status) {
+    const int t = threadIdx.x & (lanes - 1), head = C / V, all = K * head;
+    const int64_t step = (int64_t)gridDim.x * (256 / lanes);
+    for (int64_t node = (int64_t)blockIdx.x * (256 / lanes) + threadIdx.x / lanes; node < n; node += step) {
+        const int token = tok[node];
+        const bool ok = token >= 0 && token < n_tokens;
+        if (token >= n_tokens && status && t == 0) *status = E2F_ERR_INVALID_ARG;
+        const int64_t row = (int64_t)token * C, base = node * all;
+        for (int j = t; j < head; j += lanes) {
+            float v[V] = {};
+            if (ok) {
+                load_row<TT, V>(table, row + j * V, v);
                 for (int k = 0; k < V; ++k) v[k] *= scale;
-            } else if (t >= n_tokens && status) {
-                *status = E2F_ERR_INVALID_ARG;
             }
+            store_row<YT, V>(out, (base + j) * V, v);
         }
-        store_vec<YT, V>(out, row * C + c, v);
+        const float zero[V] = {};
+#pragma unroll 4
+        for (int j = head + t; j < all; j += lanes) store_row<YT, V>(out, (base + j) * V, zero);
     }
 }
 
@@ -452,12 +472,16 @@ template <int TT, int YT>
 cudaError_t launch_embed(const e2f_embed_cfg& f, const int32_t* tok, int64_t n, const void* table, void* out,
                          int* status, cudaStream_t s) {
     const int K = (f.L + 1) * (f.L + 1);
-    auto grid = [&](int v) { return (unsigned)std::min<int64_t>((n * K * (f.C / v) + 255) / 256, 148 * 64); };
+    const bool wide = f.C % kWide<YT> == 0;
+    const int V = wide ? kWide<YT> : 1;
+    int lanes = 1;  // a warp a node at most, no lanes without a value
+    while (lanes < 32 && lanes * V < K * f.C) lanes *= 2;
+    const unsigned grid = (unsigned)std::min<int64_t>((n + 256 / lanes - 1) / (256 / lanes), 148 * 32);
     count_launch();
-    if (f.C % 4 == 0)
-        k_embed<TT, YT, 4><<<grid(4), 256, 0, s>>>(tok, n, table, f.n_tokens, K, f.C, f.scale, out, status);
+    if (wide)
+        k_embed<TT, YT, kWide<YT>><<<grid, 256, 0, s>>>(tok, n, table, f.n_tokens, K, f.C, f.scale, lanes, out, status);
     else
-        k_embed<TT, YT, 1><<<grid(1), 256, 0, s>>>(tok, n, table, f.n_tokens, K, f.C, f.scale, out, status);
+        k_embed<TT, YT, 1><<<grid, 256, 0, s>>>(tok, n, table, f.n_tokens, K, f.C, f.scale, lanes, out, status);
     return cudaGetLastError();
 }
 

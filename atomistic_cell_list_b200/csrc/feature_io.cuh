@@ -57,6 +57,34 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&v)[V
     }
 }
 
+// vector i of 8 consecutive values (16-byte aligned)
+template <int T>
+__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+    if constexpr (T == kF32) {
+        const float4 a = static_cast<const float4*>(p)[2 * i], b = static_cast<const float4*>(p)[2 * i + 1];
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+        const uint4 a = static_cast<const uint4*>(p)[i];
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+        for (int k = 0; k < 4; ++k) {
+            v[2 * k] = __uint_as_float(w[k] << 16);
+            v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+    if constexpr (T == kF32) {
+        static_cast<float4*>(p)[2 * i] = make_float4(v[0], v[1], v[2], v[3]);
+        static_cast<float4*>(p)[2 * i + 1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        __nv_bfloat162 a[4];
+        for (int k = 0; k < 4; ++k) a[k] = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+        static_cast<uint4*>(p)[i] = *reinterpret_cast<uint4*>(a);
+    }
+}
+
 // fp32 value as storage type T keeps it
 template <int T>
 __device__ __forceinline__ float as_stored(float v) {
@@ -89,6 +117,13 @@ __device__ __forceinline__ uint32_t ck_code(float v, float inv) {
     return __float_as_uint(fminf(fmaxf(fmaf(v, inv, kMagic), kMagic - 127.f), kMagic + 127.f));
 }
 __device__ __forceinline__ float ck_inverse(uint32_t s) { return __uint_as_float((260u - s) << 23); }
+
+// codes of four values, first in the low byte
+__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d, float inv) {
+    const uint32_t lo = __byte_perm(ck_code(a, inv), ck_code(b, inv), 0x0040);
+    const uint32_t hi = __byte_perm(ck_code(c, inv), ck_code(d, inv), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
+}
 
 // A code as fp32, without a conversion instruction: the byte with its sign bit
 // turned over is code + 128, placed (by a byte permutation) in the low mantissa of 2^23.
@@ -180,9 +215,7 @@ __device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int6
     const float inv = ck_inverse(s);
     int8_t* q = codes + row * C + c;
     if constexpr (V == 4) {
-        const uint32_t lo = __byte_perm(ck_code(v[0], inv), ck_code(v[1], inv), 0x0040);
-        const uint32_t hi = __byte_perm(ck_code(v[2], inv), ck_code(v[3], inv), 0x0040);
-        *reinterpret_cast<uint32_t*>(q) = s == 255u ? 0u : __byte_perm(lo, hi, 0x5410);
+        *reinterpret_cast<uint32_t*>(q) = s == 255u ? 0u : pack_codes(v[0], v[1], v[2], v[3], inv);
     } else {
         for (int k = 0; k < V; ++k) q[k] = s == 255u ? 0 : (int8_t)ck_code(v[k], inv);
     }
