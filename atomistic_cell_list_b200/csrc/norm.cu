@@ -221,6 +221,74 @@ __global__ void k_norm_rows(NormArgs a) {
     }
 }
 
+// L = 0: one block per row, the row in registers, NV vectors of V values a thread.
+// All of a row's loads are in flight together; rows of other blocks of the SM hide
+// the two sums. (Reading the row once per pass, in loops: 1.1 TB/s at 4,099 rows
+// of 5,001 bf16 values.)
+template <int XT, int YT, int V, int NV>
+__global__ void __launch_bounds__(1024) k_norm_held(NormArgs a) {
+    __shared__ float sh[32];
+    const int64_t row = blockIdx.x;
+    const int T = blockDim.x, C = a.C;
+    float v[NV][V];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * T + threadIdx.x) * V;
+        for (int k = 0; k < V; ++k) v[j][k] = 0.f;
+        if (c < C) load_feat<XT, V>(a.x, a.xs, row, C, a.nb, c, v[j]);
+    }
+    if constexpr (XT != kMXI8) {
+        if (a.res) {
+            float r[NV][V];
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * T + threadIdx.x) * V;
+                for (int k = 0; k < V; ++k) r[j][k] = 0.f;
+                if (c < C) load_vec<kF32, V>(a.res, row * C + c, r[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * T + threadIdx.x) * V;
+                for (int k = 0; k < V; ++k) v[j][k] = as_stored<XT>(v[j][k] + r[j][k]);
+                if (c < C) store_vec<XT, V>(a.sum, row * C + c, v[j]);
+            }
+        }
+        if (a.codes)
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const int c = (j * T + threadIdx.x) * V;
+                store_codes<V>(a.codes, a.scales, row, C, a.nb, c, c < C, 32, v[j]);
+            }
+    }
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        for (int k = 0; k < V; ++k) s += v[j][k];
+    const float mu = block_sum(s, sh) * a.inv_c;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if ((j * T + threadIdx.x) * V < C)
+            for (int k = 0; k < V; ++k) {
+                v[j][k] -= mu;
+                q += v[j][k] * v[j][k];
+            }
+    const float r = rsqrtf(block_sum(q, sh) * a.inv_c + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * T + threadIdx.x) * V;
+        if (c >= C) continue;
+        float w[V], b[V] = {};
+        load_vec<kF32, V>(a.w, c, w);
+        if (a.b) load_vec<kF32, V>(a.b, c, b);
+        for (int k = 0; k < V; ++k) v[j][k] = fmaf(v[j][k] * r, w[k], b[k]);
+        store_vec<YT, V>(a.y, row * C + c, v[j]);
+    }
+    if (threadIdx.x == 0) {
+        if (a.mean) a.mean[row] = mu;
+        if (a.rstd) a.rstd[row] = r;
+    }
+}
+
 template <int XT, int YT, int NI>
 cudaError_t launch_teams(const NormArgs& a, const TeamPlan& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_norm_teams<XT, YT, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem);
@@ -238,6 +306,11 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
         const int vec = vec_bytes<XT>() + (a.res ? 16 : 0);
         const TeamPlan p = team_plan(a.n, a.L, a.C, vec, vec, 0, kFwdWarps);
         return p.NI == 1 ? launch_teams<XT, YT, 1>(a, p, s) : launch_teams<XT, YT, 2>(a, p, s);
+    }
+    if (a.L == 0) {  // C <= 16384 always fits
+        if (a.C % 4 == 0) k_norm_held<XT, YT, 4, 4><<<(unsigned)a.n, held_threads(a.C, 4, 4), 0, s>>>(a);
+        else k_norm_held<XT, YT, 1, 16><<<(unsigned)a.n, held_threads(a.C, 1, 16), 0, s>>>(a);
+        return cudaGetLastError();
     }
     const unsigned grid = (unsigned)std::min<int64_t>(a.n * (a.L + 1), 1 << 20);
     if (a.C % 4 == 0) k_norm_rows<XT, YT, 4><<<grid, row_threads(a.C, 4), 0, s>>>(a);

@@ -20,7 +20,8 @@
 // shared memory, one to three units ahead of the one in work. Warps never wait for
 // one another, and the bytes in flight (about 100 KB an SM) do not depend on
 // registers or occupancy. Lanes beyond the row read zeros.
-// Any other C: one block per (node, degree).
+// L = 0 with any other C: one block per row, the row in registers. The rest: one
+// block per (node, degree), which reads its group once per pass.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -200,6 +201,12 @@ __device__ __forceinline__ float block_sum(float v, float* sh) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     return v;
+}
+
+// threads for rows of C values held in registers, nv vectors of v each; 0: the row is too long
+int held_threads(int C, int v, int nv, int most = 1024) {
+    const int t = ((C + v * nv - 1) / (v * nv) + 31) / 32 * 32;
+    return t <= most ? t : 0;
 }
 
 int row_threads(int C, int V) {

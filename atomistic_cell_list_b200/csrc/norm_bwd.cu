@@ -226,6 +226,63 @@ __global__ void k_norm_bwd_rows(NormBwdArgs a) {
         }
 }
 
+// L = 0: persistent blocks, one row at a time in registers, NV vectors of V values
+// of x and of grad_y a thread, with the weight and bias gradient of its channels.
+// part: [block][C], then [block][C] for the bias.
+template <int XT, int V, int NV>
+__global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_norm_bwd_held(NormBwdArgs a) {
+    __shared__ float sh[2][32];
+    const int T = blockDim.x, C = a.C;
+    float dw[NV][V] = {}, db[NV][V] = {};
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        float x[NV][V], g[NV][V], s1 = 0.f, s2 = 0.f;
+        const float mu = a.mean[row], r = a.rstd[row];
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * T + threadIdx.x) * V;
+            for (int k = 0; k < V; ++k) x[j][k] = g[j][k] = 0.f;
+            if (c < C) {
+                load_feat<XT, V>(a.x, a.xs, row, C, a.nb, c, x[j]);
+                load_vec<kF32, V>(a.gy, row * C + c, g[j]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * T + threadIdx.x) * V;
+            if (c >= C) continue;
+            float w[V];
+            load_vec<kF32, V>(a.w, c, w);
+            for (int k = 0; k < V; ++k) {
+                const float xh = (x[j][k] - mu) * r, u = g[j][k] * w[k];
+                dw[j][k] += g[j][k] * xh;
+                db[j][k] += g[j][k];
+                s1 += u;
+                s2 += u * xh;
+                x[j][k] = xh;
+                g[j][k] = u;
+            }
+        }
+        const float m1 = block_sum(s1, sh[0]) * a.inv_c, m2 = block_sum(s2, sh[1]) * a.inv_c;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int c = (j * T + threadIdx.x) * V;
+            if (c >= C) continue;
+            float e[V] = {};
+            if (a.skip) load_vec<kF32, V>(a.skip, row * C + c, e);
+            for (int k = 0; k < V; ++k) e[k] += r * (g[j][k] - m1 - x[j][k] * m2);
+            store_vec<kF32, V>(a.gx, row * C + c, e);
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int c = (j * T + threadIdx.x) * V;
+        if (c >= C) continue;
+        store_vec<kF32, V>(a.part, (int64_t)blockIdx.x * C + c, dw[j]);
+        store_vec<kF32, V>(a.part, (int64_t)(gridDim.x + blockIdx.x) * C + c, db[j]);
+    }
+}
+
 // Sums the blocks' partials: `count` rows of `stride` values for each degree and the bias.
 struct JoinPlan {
     int64_t base[kMaxL + 2], stride;
@@ -274,9 +331,14 @@ cudaError_t launch_bwd_teams(const NormBwdArgs& a, const TeamPlan& p, cudaStream
     return cudaGetLastError();
 }
 
-// blocks per row of features of k_norm_bwd_rows
-int rows_blocks(int64_t n, int L) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>(n, kNormBlocks / ((L + 1) * (L + 1))));
+// threads of k_norm_bwd_held, 0: not for this shape
+int bwd_held(int L, int C) { return L ? 0 : C % 4 == 0 ? held_threads(C, 4, 2) : held_threads(C, 1, 16, 512); }
+
+// blocks of k_norm_bwd_held (about 1,024 threads an SM: more partials would cost
+// more than they hide), or blocks per row of features of k_norm_bwd_rows
+int rows_blocks(int64_t n, int L, int C) {
+    const int t = bwd_held(L, C), most = t ? kSMs * std::max(1, std::min(8, 1024 / t)) : kNormBlocks / ((L + 1) * (L + 1));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n, most));
 }
 
 template <int XT>
@@ -295,8 +357,13 @@ cudaError_t launch_bwd(NormBwdArgs a, float* gw, float* gb, cudaStream_t s) {
             j.count[l] = l <= a.L ? p.at[l + 1] - p.at[l] : p.at[1];
         }
     } else {
-        a.g = rows_blocks(a.n, a.L);
-        e = a.C % 4 == 0 ? launch_bwd_rows<XT, 4>(a, s) : launch_bwd_rows<XT, 1>(a, s);
+        a.g = rows_blocks(a.n, a.L, a.C);
+        if (const int t = bwd_held(a.L, a.C)) {
+            if (a.C % 4 == 0) k_norm_bwd_held<XT, 4, 2><<<a.g, t, 0, s>>>(a);
+            else k_norm_bwd_held<XT, 1, 16><<<a.g, t, 0, s>>>(a);
+            e = cudaGetLastError();
+        } else
+            e = a.C % 4 == 0 ? launch_bwd_rows<XT, 4>(a, s) : launch_bwd_rows<XT, 1>(a, s);
         j.stride = a.C;
         for (int l = 0; l < a.L + 2; ++l) {
             j.base[l] = (int64_t)a.g * (l <= a.L ? l * l : K) * a.C;
@@ -318,7 +385,7 @@ extern "C" size_t e2f_layer_norm_backward_workspace_size(int64_t n_atoms, const 
     if (check_norm_cfg(cfg) != E2F_OK || n_atoms < 0) return 0;
     if (n_atoms == 0) return 256;
     if (use_teams(cfg->C)) return align_up(4 * (size_t)(2 * (kTeamBlocks + kMaxL)) * cfg->C, 256);
-    return align_up(4 * (size_t)rows_blocks(n_atoms, cfg->L) * ((cfg->L + 1) * (cfg->L + 1) + 1) * cfg->C, 256);
+    return align_up(4 * (size_t)rows_blocks(n_atoms, cfg->L, cfg->C) * ((cfg->L + 1) * (cfg->L + 1) + 1) * cfg->C, 256);
 }
 
 extern "C" e2f_status e2f_layer_norm_backward(const e2f_norm_cfg* cfg, int64_t n_atoms, const void* x,
