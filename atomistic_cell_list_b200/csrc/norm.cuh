@@ -9,7 +9,7 @@
 //   grad_weight[l,c] = sum_{n,m} grad_y xh,   grad_bias[c] = sum_n grad_y[n,0,c]
 // All sums are fp32. A few operations per value: memory bound.
 //
-// C a multiple of 16 up to 256 (what the attention takes): a team of TL lanes (a
+// C a multiple of 4 up to 256 (the attention takes multiples of 16): a team of TL lanes (a
 // power of two, TL >= C/4 up to 32) owns whole rows, lane t the channels
 // 4 (t + TL i) .. +3, i < NI. A block works on one degree, so that its code has the
 // rows of a group unrolled and stays in the instruction cache (with all degrees in
@@ -94,7 +94,7 @@ struct Slots {
     int stage_bytes, stages, o1, o2, o3, at[kMaxL + 2];
 };
 
-bool use_teams(int C) { return C % 16 == 0 && C <= kTeamC; }
+bool use_teams(int C) { return C % 4 == 0 && C <= kTeamC; }
 
 // bytes of 4 channels
 template <int T>
@@ -129,8 +129,9 @@ TeamPlan team_plan(int64_t n, int L, int C, int vec, int most, int small, int ca
 __device__ __forceinline__ void cp_async16(uint32_t to, const void* from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t to, const void* from) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+template <int BYTES>  // 4 or 8
+__device__ __forceinline__ void cp_async_small(uint32_t to, const void* from) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // all but the newest n groups of this thread have arrived
@@ -153,13 +154,31 @@ struct Unit {
         const int64_t left = n - first;
         have = left <= 0 ? 0 : left >= B * teams ? B : (int)(left + teams - 1) / teams;
     }
-    // starts the copies of one stream [rows, C] of storage T to `to`: [team][node][row][C]
+    // starts the copies of one stream [rows, C] of storage T to `to`: [team][node][row][C],
+    // in 16-byte pieces, or vector by vector where rows do not begin on 16 bytes
     template <int T>
     __device__ __forceinline__ void fetch(const void* p, int C, int K, int TL, uint32_t to) const {
         constexpr int IT = (R * NI * vec_bytes<T>() + 15) / 16;
         const int lane = threadIdx.x & 31, t16 = (lane & (TL - 1)) * 16, bytes = R * C * (vec_bytes<T>() / 4);
         const char* q = static_cast<const char*>(p) + row0 * C * (vec_bytes<T>() / 4) + t16;
         to += lane / TL * (B * bytes) + t16;
+        if constexpr (T != kF32)
+            if (C * (vec_bytes<T>() / 4) % 16) {
+                constexpr int VB = vec_bytes<T>();
+                const int t = lane & (TL - 1);
+                q += t * VB - t16;
+                to += t * VB - t16;
+                for (int b = 0; b < have; ++b) {
+                    for (int o = 0; o < R; ++o)
+#pragma unroll
+                        for (int i = 0; i < NI; ++i)
+                            if ((t + TL * i) * 4 < C)
+                                cp_async_small<VB>(to + (o * (C / 4) + TL * i) * VB, q + (o * (C / 4) + TL * i) * VB);
+                    q += (int64_t)(32 / TL * K) * C * (VB / 4);
+                    to += bytes;
+                }
+                return;
+            }
 #pragma unroll
         for (int b = 0; b < B; ++b)
             if (b < have) {

@@ -43,8 +43,8 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
             to += sl.o3 + 4 * team * B;  // statistics: [team][node] rstd, then mean
             for (int b = t; b < u.have; b += TL) {
                 const int64_t node = u.first + b * teams;
-                cp_async4(to + 4 * b, a.rstd + node * (a.L + 1) + l);
-                if (l == 0) cp_async4(to + 4 * (kStatNodes + b), a.mean + node);
+                cp_async_small<4>(to + 4 * b, a.rstd + node * (a.L + 1) + l);
+                if (l == 0) cp_async_small<4>(to + 4 * (kStatNodes + b), a.mean + node);
             }
         }
         cp_commit();
