@@ -307,6 +307,7 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
         const TeamPlan p = team_plan(a.n, a.L, a.C, vec, vec, 0, kFwdWarps);
         return p.NI == 1 ? launch_teams<XT, YT, 1>(a, p, s) : launch_teams<XT, YT, 2>(a, p, s);
     }
+    if (a.C <= kTeamC) return run_norm_scalar(a, XT, YT == kBF16, s);
     if (a.L == 0) {  // C <= 16384 always fits
         if (a.C % 4 == 0) k_norm_held<XT, YT, 4, 4><<<(unsigned)a.n, held_threads(a.C, 4, 4), 0, s>>>(a);
         else k_norm_held<XT, YT, 1, 16><<<(unsigned)a.n, held_threads(a.C, 1, 16), 0, s>>>(a);

@@ -20,7 +20,8 @@
 // shared memory, one to three units ahead of the one in work. Warps never wait for
 // one another, and the bytes in flight (about 100 KB an SM) do not depend on
 // registers or occupancy. Lanes beyond the row read zeros.
-// L = 0 with any other C: one block per row, the row in registers. The rest: one
+// Other C up to 256: one warp per unit, values one by one (norm_scalar.cu).
+// L = 0 with more channels: one block per row, the row in registers. The rest: one
 // block per (node, degree), which reads its group once per pass.
 #pragma once
 
@@ -34,11 +35,6 @@
 #include "feature_io.cuh"
 
 namespace e2f {
-namespace {
-
-constexpr int kMaxNormC = 16384;
-constexpr int kNormBlocks = 592;  // most blocks of a weight-gradient pass: 4 on each of 148 SMs
-
 struct NormArgs {
     int64_t n;
     int L, C, nb;
@@ -71,6 +67,15 @@ struct NormBwdArgs {
     float* part;  // weight-gradient partials (null: not wanted)
     int g;        // k_norm_bwd_rows: degree l has g (2l+1) blocks
 };
+
+// up to 256 channels, any number: norm_scalar.cu. at: the blocks of degree l are [at[l], at[l+1]), at[0] = 0.
+cudaError_t run_norm_scalar(const NormArgs& a, int x_type, bool y_bf16, cudaStream_t s);
+cudaError_t run_norm_bwd_scalar(const NormBwdArgs& a, int x_type, int* at, cudaStream_t s);
+
+namespace {
+
+constexpr int kMaxNormC = 16384;
+constexpr int kNormBlocks = 592;  // most blocks of a weight-gradient pass: 4 on each of 148 SMs
 
 constexpr int kSMs = 148;
 constexpr int kTeamC = 256;  // most channels a team holds

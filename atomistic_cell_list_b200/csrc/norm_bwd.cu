@@ -346,16 +346,23 @@ cudaError_t launch_bwd(NormBwdArgs a, float* gw, float* gb, cudaStream_t s) {
     const int K = (a.L + 1) * (a.L + 1);
     JoinPlan j{};
     cudaError_t e;
+    auto join_degrees = [&](const int* at) {  // blocks of one degree, then the bias of those of degree 0
+        j.stride = a.C;
+        for (int l = 0; l < a.L + 2; ++l) {
+            j.base[l] = (int64_t)(l <= a.L ? at[l] : at[kMaxL + 1]) * a.C;
+            j.count[l] = l <= a.L ? at[l + 1] - at[l] : at[1];
+        }
+    };
     count_launch();
     if (use_teams(a.C)) {
         const TeamPlan p = team_plan(a.n, a.L, a.C, vec_bytes<XT>() + (a.skip ? 32 : 16), vec_bytes<XT>() + 32,
                                      kStatBytes, kBwdWarps);
         e = p.NI == 1 ? launch_bwd_teams<XT, 1>(a, p, s) : launch_bwd_teams<XT, 2>(a, p, s);
-        j.stride = a.C;
-        for (int l = 0; l < a.L + 2; ++l) {
-            j.base[l] = (int64_t)(l <= a.L ? p.at[l] : p.at[kMaxL + 1]) * a.C;
-            j.count[l] = l <= a.L ? p.at[l + 1] - p.at[l] : p.at[1];
-        }
+        join_degrees(p.at);
+    } else if (a.C <= kTeamC) {
+        int at[kMaxL + 2];
+        e = run_norm_bwd_scalar(a, XT, at, s);
+        join_degrees(at);
     } else {
         a.g = rows_blocks(a.n, a.L, a.C);
         if (const int t = bwd_held(a.L, a.C)) {
@@ -384,7 +391,7 @@ using namespace e2f;
 extern "C" size_t e2f_layer_norm_backward_workspace_size(int64_t n_atoms, const e2f_norm_cfg* cfg) {
     if (check_norm_cfg(cfg) != E2F_OK || n_atoms < 0) return 0;
     if (n_atoms == 0) return 256;
-    if (use_teams(cfg->C)) return align_up(4 * (size_t)(2 * (kTeamBlocks + kMaxL)) * cfg->C, 256);
+    if (cfg->C <= kTeamC) return align_up(4 * (size_t)(2 * (kTeamBlocks + kMaxL)) * cfg->C, 256);
     return align_up(4 * (size_t)rows_blocks(n_atoms, cfg->L, cfg->C) * ((cfg->L + 1) * (cfg->L + 1) + 1) * cfg->C, 256);
 }
 
