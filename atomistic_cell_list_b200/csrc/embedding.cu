@@ -112,10 +112,29 @@ __device__ __forceinline__ uint32_t sort_key(int t, int n_tokens) {
     return t < 0 || t >= n_tokens ? (uint32_t)n_tokens : (uint32_t)t;
 }
 
+// What the kernels of the sort do beside it: zeros for the whole table, a share
+// in each kernel, by blocks behind those that sort. The sort is bound by latency,
+// the zeros by the memory.
+struct Zeros {
+    float* to;
+    int64_t from, n;  // values; from is a multiple of 4
+};
+constexpr int kZeroBlocks = 148;
+// true in the blocks behind the first `blocks`, which write their part of the zeros
+__device__ __forceinline__ bool zero_blocks(const Zeros& z, int64_t blocks) {
+    if ((int64_t)blockIdx.x < blocks) return false;
+    const int64_t t = (blockIdx.x - blocks) * 256 + threadIdx.x;
+    float4* to = reinterpret_cast<float4*>(z.to + z.from);
+    for (int64_t i = t; i < z.n / 4; i += kZeroBlocks * 256) to[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (t < z.n % 4) z.to[z.from + z.n / 4 * 4 + t] = 0.f;
+    return true;
+}
+
 // digit counts of one tile: hist[digit][tile]
 template <bool FIRST>
 __global__ void __launch_bounds__(256) k_sort_count(const void* keys, int64_t n, int n_tokens, int shift,
-                                                    int64_t tiles, uint32_t* hist, int* status) {
+                                                    int64_t tiles, uint32_t* hist, int* status, Zeros z) {
+    if (zero_blocks(z, tiles)) return;
     __shared__ uint32_t cnt[256];
     cnt[threadIdx.x] = 0;
     __syncthreads();
@@ -138,7 +157,8 @@ __global__ void __launch_bounds__(256) k_sort_count(const void* keys, int64_t n,
 }
 
 // block d: exclusive prefix over the tiles of digit d, in place; its total
-__global__ void __launch_bounds__(256) k_sort_scan(uint32_t* hist, int64_t tiles, uint32_t* total) {
+__global__ void __launch_bounds__(256) k_sort_scan(uint32_t* hist, int64_t tiles, uint32_t* total, Zeros z) {
+    if (zero_blocks(z, 256)) return;
     __shared__ uint32_t ws[8];
     uint32_t* h = hist + blockIdx.x * tiles;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -169,7 +189,8 @@ __global__ void __launch_bounds__(256) k_sort_scan(uint32_t* hist, int64_t tiles
 template <bool FIRST>
 __global__ void __launch_bounds__(256) k_sort_place(const void* keys, const int* idx, int64_t n, int n_tokens,
                                                     int shift, int64_t tiles, const uint32_t* hist,
-                                                    const uint32_t* total, uint32_t* keys_out, int* idx_out) {
+                                                    const uint32_t* total, uint32_t* keys_out, int* idx_out, Zeros z) {
+    if (zero_blocks(z, tiles)) return;
     constexpr int J = kSortTile / 256;
     __shared__ uint32_t wc[8][256];
     __shared__ uint32_t ws[8];
@@ -390,7 +411,7 @@ __global__ void __launch_bounds__(256) k_run_sum(RunArgs a) {
             if (cur < n_tokens && in)
                 store_vec<kF32, V>(a.part, (2 * (int64_t)blockIdx.x + (begins ? 1 : 0)) * a.C + c, acc);
         };
-        for (int q = 0; q < 2 * teams; ++q) {
+        for (int q = 0; q < 2 * ((n + per - 1) / per); ++q) {  // the teams that had tokens
             const uint32_t key = ent_key[q >> 1][q & 1];
             if (key == none) continue;
             if (key != cur) {
@@ -513,21 +534,28 @@ cudaError_t run_embed_bwd(const e2f_embed_cfg& f, const int32_t* tok, int64_t n,
         key[k] = reinterpret_cast<uint32_t*>(ws + w.o_key[k]);
         idx[k] = reinterpret_cast<int*>(ws + w.o_idx[k]);
     }
-    cudaError_t e = cudaMemsetAsync(grad, 0, 4 * (size_t)f.n_tokens * f.C, s);
-    if (e != cudaSuccess) return e;
     const unsigned tiles = (unsigned)w.sort_tiles;
+    const int64_t values = (int64_t)f.n_tokens * f.C, share = (values / (3 * w.passes) + 4095) / 4096 * 4096;
+    int64_t zeroed = 0;
+    auto zeros = [&]() {  // the next share, the rest in the last kernel's
+        const Zeros z{grad, zeroed, std::min(share, values - zeroed)};
+        zeroed += z.n;
+        return z;
+    };
     for (int p = 0; p < w.passes; ++p) {
         const int to = p & 1, from = to ^ 1;
         if (p == 0) {
-            k_sort_count<true><<<tiles, 256, 0, s>>>(tok, n, f.n_tokens, 0, w.sort_tiles, hist, status);
-            k_sort_scan<<<256, 256, 0, s>>>(hist, w.sort_tiles, total);
-            k_sort_place<true><<<tiles, 256, 0, s>>>(tok, nullptr, n, f.n_tokens, 0, w.sort_tiles, hist, total, key[to],
-                                                     idx[to]);
+            k_sort_count<true><<<tiles + kZeroBlocks, 256, 0, s>>>(tok, n, f.n_tokens, 0, w.sort_tiles, hist, status,
+                                                                   zeros());
+            k_sort_scan<<<256 + kZeroBlocks, 256, 0, s>>>(hist, w.sort_tiles, total, zeros());
+            k_sort_place<true><<<tiles + kZeroBlocks, 256, 0, s>>>(tok, nullptr, n, f.n_tokens, 0, w.sort_tiles, hist,
+                                                                   total, key[to], idx[to], zeros());
         } else {
-            k_sort_count<false><<<tiles, 256, 0, s>>>(key[from], n, f.n_tokens, 8 * p, w.sort_tiles, hist, nullptr);
-            k_sort_scan<<<256, 256, 0, s>>>(hist, w.sort_tiles, total);
-            k_sort_place<false><<<tiles, 256, 0, s>>>(key[from], idx[from], n, f.n_tokens, 8 * p, w.sort_tiles, hist,
-                                                      total, key[to], idx[to]);
+            k_sort_count<false><<<tiles + kZeroBlocks, 256, 0, s>>>(key[from], n, f.n_tokens, 8 * p, w.sort_tiles, hist,
+                                                                    nullptr, zeros());
+            k_sort_scan<<<256 + kZeroBlocks, 256, 0, s>>>(hist, w.sort_tiles, total, zeros());
+            k_sort_place<false><<<tiles + kZeroBlocks, 256, 0, s>>>(key[from], idx[from], n, f.n_tokens, 8 * p,
+                                                                    w.sort_tiles, hist, total, key[to], idx[to], zeros());
         }
         count_launch(3);
     }

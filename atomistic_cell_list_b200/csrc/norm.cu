@@ -223,65 +223,71 @@ __global__ void k_norm_rows(NormArgs a) {
 
 // L = 0: one block per row, the row in registers, NV vectors of V values a thread.
 // All of a row's loads are in flight together; rows of other blocks of the SM hide
-// the two sums. (Reading the row once per pass, in loops: 1.1 TB/s at 4,099 rows
-// of 5,001 bf16 values.)
-template <int XT, int YT, int V, int NV>
-__global__ void __launch_bounds__(1024) k_norm_held(NormArgs a) {
+// the two sums. TT > 0: that many threads, so that the offsets of a thread's values
+// are constants (value by value, the instructions bound it: 55 a value became 20).
+template <int XT, int YT, int V, int NV, int TT>
+__global__ void __launch_bounds__(TT ? TT : 1024) k_norm_held(NormArgs a) {
     __shared__ float sh[32];
-    const int64_t row = blockIdx.x;
-    const int T = blockDim.x, C = a.C;
+    const int64_t row = blockIdx.x, base = row * a.C + threadIdx.x * V;
+    const int T = TT ? TT : blockDim.x, C = a.C - threadIdx.x * V;  // this thread's vector j exists: j T V < C
+    const char* x = static_cast<const char*>(a.x) + base * (vec_bytes<XT>() / 4);
     float v[NV][V];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * T + threadIdx.x) * V;
         for (int k = 0; k < V; ++k) v[j][k] = 0.f;
-        if (c < C) load_feat<XT, V>(a.x, a.xs, row, C, a.nb, c, v[j]);
+        if (j * T * V < C) {
+            if constexpr (XT == kMXI8)
+                load_codes<V>(static_cast<const int8_t*>(a.x), a.xs, row, a.C, a.nb, (j * T + threadIdx.x) * V, v[j]);
+            else
+                load_vec<XT, V>(x, j * T * V, v[j]);
+        }
     }
     if constexpr (XT != kMXI8) {
         if (a.res) {
             float r[NV][V];
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * T + threadIdx.x) * V;
                 for (int k = 0; k < V; ++k) r[j][k] = 0.f;
-                if (c < C) load_vec<kF32, V>(a.res, row * C + c, r[j]);
+                if (j * T * V < C) load_vec<kF32, V>(a.res + base, j * T * V, r[j]);
             }
+            char* sum = static_cast<char*>(a.sum) + base * (vec_bytes<XT>() / 4);
 #pragma unroll
             for (int j = 0; j < NV; ++j) {
-                const int c = (j * T + threadIdx.x) * V;
                 for (int k = 0; k < V; ++k) v[j][k] = as_stored<XT>(v[j][k] + r[j][k]);
-                if (c < C) store_vec<XT, V>(a.sum, row * C + c, v[j]);
+                if (j * T * V < C) store_vec<XT, V>(sum, j * T * V, v[j]);
             }
         }
         if (a.codes)
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const int c = (j * T + threadIdx.x) * V;
-                store_codes<V>(a.codes, a.scales, row, C, a.nb, c, c < C, 32, v[j]);
-            }
+            for (int j = 0; j < NV; ++j)
+                store_codes<V>(a.codes, a.scales, row, a.C, a.nb, (j * T + threadIdx.x) * V, j * T * V < C, 32, v[j]);
     }
-    float s = 0.f, q = 0.f;
+    float s = 0.f, q = 0.f, w[NV][V], b[NV][V];  // the weights arrive while the sums are formed
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        for (int k = 0; k < V; ++k) w[j][k] = b[j][k] = 0.f;
+        if (j * T * V < C) {
+            load_vec<kF32, V>(a.w + threadIdx.x * V, j * T * V, w[j]);
+            if (a.b) load_vec<kF32, V>(a.b + threadIdx.x * V, j * T * V, b[j]);
+        }
+    }
 #pragma unroll
     for (int j = 0; j < NV; ++j)
         for (int k = 0; k < V; ++k) s += v[j][k];
     const float mu = block_sum(s, sh) * a.inv_c;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-        if ((j * T + threadIdx.x) * V < C)
+        if (j * T * V < C)
             for (int k = 0; k < V; ++k) {
                 v[j][k] -= mu;
                 q += v[j][k] * v[j][k];
             }
     const float r = rsqrtf(block_sum(q, sh) * a.inv_c + a.eps);
+    char* y = static_cast<char*>(a.y) + base * (vec_bytes<YT>() / 4);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        const int c = (j * T + threadIdx.x) * V;
-        if (c >= C) continue;
-        float w[V], b[V] = {};
-        load_vec<kF32, V>(a.w, c, w);
-        if (a.b) load_vec<kF32, V>(a.b, c, b);
-        for (int k = 0; k < V; ++k) v[j][k] = fmaf(v[j][k] * r, w[k], b[k]);
-        store_vec<YT, V>(a.y, row * C + c, v[j]);
+        for (int k = 0; k < V; ++k) v[j][k] = fmaf(v[j][k] * r, w[j][k], b[j][k]);
+        if (j * T * V < C) store_vec<YT, V>(y, j * T * V, v[j]);
     }
     if (threadIdx.x == 0) {
         if (a.mean) a.mean[row] = mu;
@@ -309,8 +315,11 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
     }
     if (a.C <= kTeamC) return run_norm_scalar(a, XT, YT == kBF16, s);
     if (a.L == 0) {  // C <= 16384 always fits
-        if (a.C % 4 == 0) k_norm_held<XT, YT, 4, 4><<<(unsigned)a.n, held_threads(a.C, 4, 4), 0, s>>>(a);
-        else k_norm_held<XT, YT, 1, 16><<<(unsigned)a.n, held_threads(a.C, 1, 16), 0, s>>>(a);
+        const unsigned grid = (unsigned)a.n;
+        if (a.C % 4 == 0) k_norm_held<XT, YT, 4, 4, 0><<<grid, held_threads(a.C, 4, 4), 0, s>>>(a);
+        else if (a.C <= 1024) k_norm_held<XT, YT, 1, 8, 128><<<grid, 128, 0, s>>>(a);
+        else if (a.C <= 6144) k_norm_held<XT, YT, 1, 16, 384><<<grid, 384, 0, s>>>(a);
+        else k_norm_held<XT, YT, 1, 16, 1024><<<grid, 1024, 0, s>>>(a);
         return cudaGetLastError();
     }
     const unsigned grid = (unsigned)std::min<int64_t>(a.n * (a.L + 1), 1 << 20);

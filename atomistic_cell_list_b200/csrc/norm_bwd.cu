@@ -229,58 +229,63 @@ __global__ void k_norm_bwd_rows(NormBwdArgs a) {
 // L = 0: persistent blocks, one row at a time in registers, NV vectors of V values
 // of x and of grad_y a thread, with the weight and bias gradient of its channels.
 // part: [block][C], then [block][C] for the bias.
-template <int XT, int V, int NV>
-__global__ void __launch_bounds__(V == 4 ? 1024 : 512) k_norm_bwd_held(NormBwdArgs a) {
+template <int XT, int V, int NV, int TT>
+__global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a) {
     __shared__ float sh[2][32];
-    const int T = blockDim.x, C = a.C;
+    const int T = TT ? TT : blockDim.x, C = a.C - threadIdx.x * V;  // this thread's vector j exists: j T V < C
     float dw[NV][V] = {}, db[NV][V] = {};
+    const float* wp = a.w + threadIdx.x * V;
     for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C + threadIdx.x * V;
+        const char* xp = static_cast<const char*>(a.x) + base * (vec_bytes<XT>() / 4);
+        const float *gp = a.gy + base, *kp = a.skip + base;
+        float* op = a.gx + base;
         float x[NV][V], g[NV][V], s1 = 0.f, s2 = 0.f;
         const float mu = a.mean[row], r = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int c = (j * T + threadIdx.x) * V;
             for (int k = 0; k < V; ++k) x[j][k] = g[j][k] = 0.f;
-            if (c < C) {
-                load_feat<XT, V>(a.x, a.xs, row, C, a.nb, c, x[j]);
-                load_vec<kF32, V>(a.gy, row * C + c, g[j]);
+            if (j * T * V < C) {
+                if constexpr (XT == kMXI8)
+                    load_codes<V>(static_cast<const int8_t*>(a.x), a.xs, row, a.C, a.nb, (j * T + threadIdx.x) * V, x[j]);
+                else
+                    load_vec<XT, V>(xp, j * T * V, x[j]);
+                load_vec<kF32, V>(gp, j * T * V, g[j]);
             }
         }
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * T + threadIdx.x) * V;
-            if (c >= C) continue;
-            float w[V];
-            load_vec<kF32, V>(a.w, c, w);
-            for (int k = 0; k < V; ++k) {
-                const float xh = (x[j][k] - mu) * r, u = g[j][k] * w[k];
-                dw[j][k] += g[j][k] * xh;
-                db[j][k] += g[j][k];
-                s1 += u;
-                s2 += u * xh;
-                x[j][k] = xh;
-                g[j][k] = u;
+        for (int j = 0; j < NV; ++j)
+            if (j * T * V < C) {
+                float w[V];
+                load_vec<kF32, V>(wp, j * T * V, w);
+                for (int k = 0; k < V; ++k) {
+                    const float xh = (x[j][k] - mu) * r, u = g[j][k] * w[k];
+                    dw[j][k] += g[j][k] * xh;
+                    db[j][k] += g[j][k];
+                    s1 += u;
+                    s2 += u * xh;
+                    x[j][k] = xh;
+                    g[j][k] = u;
+                }
             }
-        }
         const float m1 = block_sum(s1, sh[0]) * a.inv_c, m2 = block_sum(s2, sh[1]) * a.inv_c;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const int c = (j * T + threadIdx.x) * V;
-            if (c >= C) continue;
-            float e[V] = {};
-            if (a.skip) load_vec<kF32, V>(a.skip, row * C + c, e);
-            for (int k = 0; k < V; ++k) e[k] += r * (g[j][k] - m1 - x[j][k] * m2);
-            store_vec<kF32, V>(a.gx, row * C + c, e);
-        }
+        for (int j = 0; j < NV; ++j)
+            if (j * T * V < C) {
+                float e[V] = {};
+                if (a.skip) load_vec<kF32, V>(kp, j * T * V, e);
+                for (int k = 0; k < V; ++k) e[k] += r * (g[j][k] - m1 - x[j][k] * m2);
+                store_vec<kF32, V>(op, j * T * V, e);
+            }
     }
     if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * a.C + threadIdx.x * V;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int c = (j * T + threadIdx.x) * V;
-        if (c >= C) continue;
-        store_vec<kF32, V>(a.part, (int64_t)blockIdx.x * C + c, dw[j]);
-        store_vec<kF32, V>(a.part, (int64_t)(gridDim.x + blockIdx.x) * C + c, db[j]);
-    }
+    for (int j = 0; j < NV; ++j)
+        if (j * T * V < C) {
+            store_vec<kF32, V>(part, j * T * V, dw[j]);
+            store_vec<kF32, V>(part + (int64_t)gridDim.x * a.C, j * T * V, db[j]);
+        }
 }
 
 // Sums the blocks' partials: `count` rows of `stride` values for each degree and the bias.
@@ -332,7 +337,11 @@ cudaError_t launch_bwd_teams(const NormBwdArgs& a, const TeamPlan& p, cudaStream
 }
 
 // threads of k_norm_bwd_held, 0: not for this shape
-int bwd_held(int L, int C) { return L ? 0 : C % 4 == 0 ? held_threads(C, 4, 2) : held_threads(C, 1, 16, 512); }
+int bwd_held(int L, int C) {
+    if (L) return 0;
+    if (C % 4 == 0) return held_threads(C, 4, 2);
+    return C <= 1024 ? 128 : C <= 6144 ? 512 : 0;
+}
 
 // blocks of k_norm_bwd_held (about 1,024 threads an SM: more partials would cost
 // more than they hide), or blocks per row of features of k_norm_bwd_rows
@@ -366,8 +375,9 @@ cudaError_t launch_bwd(NormBwdArgs a, float* gw, float* gb, cudaStream_t s) {
     } else {
         a.g = rows_blocks(a.n, a.L, a.C);
         if (const int t = bwd_held(a.L, a.C)) {
-            if (a.C % 4 == 0) k_norm_bwd_held<XT, 4, 2><<<a.g, t, 0, s>>>(a);
-            else k_norm_bwd_held<XT, 1, 16><<<a.g, t, 0, s>>>(a);
+            if (a.C % 4 == 0) k_norm_bwd_held<XT, 4, 2, 0><<<a.g, t, 0, s>>>(a);
+            else if (t == 128) k_norm_bwd_held<XT, 1, 8, 128><<<a.g, t, 0, s>>>(a);
+            else k_norm_bwd_held<XT, 1, 12, 512><<<a.g, t, 0, s>>>(a);
             e = cudaGetLastError();
         } else
             e = a.C % 4 == 0 ? launch_bwd_rows<XT, 4>(a, s) : launch_bwd_rows<XT, 1>(a, s);
