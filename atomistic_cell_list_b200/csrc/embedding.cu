@@ -370,12 +370,18 @@ __global__ void __launch_bounds__(256) k_run_sum(RunArgs a) {
         for (int p = p0; p < p1; p += U) {
             uint32_t key[U];
             float v[U][V];
+            // every load is made, so that all are in flight: padding and what lies behind the part read the
+            // batch's first row, lanes beyond the columns the first column, and count as zero
 #pragma unroll
             for (int j = 0; j < U; ++j) {
-                key[j] = p + j < p1 ? keys[p + j] : n_tokens;
-                for (int k = 0; k < V; ++k) v[j][k] = 0.f;
-                if (key[j] < n_tokens && in) load_vec<kF32, V>(a.g, idx[p + j] * a.row_stride + c, v[j]);
+                const int at = p + j < p1 ? p + j : p;
+                key[j] = keys[at];
+                load_vec<kF32, V>(a.g, idx[at] * a.row_stride + (in ? c : 0), v[j]);
             }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+                if (key[j] >= n_tokens)
+                    for (int k = 0; k < V; ++k) v[j][k] = 0.f;
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 if (p + j >= p1) break;
@@ -453,14 +459,26 @@ template <int V>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_token_join(RunArgs a, int64_t tiles) {
     const int key = blockIdx.x, c = (blockIdx.y * 32 + (threadIdx.x & 31)) * V;
     float acc[V] = {};
-    if (c < a.C)
-#pragma unroll 4
-        for (int64_t b = threadIdx.x >> 5; b < tiles; b += kJoinWarps)
-            if (a.has[b * a.n_tokens + key]) {
-                float v[V];
-                load_vec<kF32, V>(a.part, (b * a.n_tokens + key) * a.C + c, v);
-                for (int k = 0; k < V; ++k) acc[k] += v[k];
-            }
+    constexpr int U = 8;  // tiles whose sums are loaded together; those without the token are loaded and not used
+    for (int64_t b0 = threadIdx.x >> 5; b0 < tiles; b0 += U * kJoinWarps) {
+        bool has[U];
+        bool any = false;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t b = b0 + j * kJoinWarps;
+            has[j] = a.has[min(b, tiles - 1) * a.n_tokens + key] && b < tiles;
+            any |= has[j];
+        }
+        if (!any || c >= a.C) continue;
+        float v[U][V];
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            load_vec<kF32, V>(a.part, (min(b0 + j * kJoinWarps, tiles - 1) * a.n_tokens + key) * a.C + c, v[j]);
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (has[j])
+                for (int k = 0; k < V; ++k) acc[k] += v[j][k];
+    }
     if (!join_warps<V>(acc) || c >= a.C) return;
     for (int k = 0; k < V; ++k) acc[k] *= a.scale;
     store_vec<kF32, V>(a.grad, (int64_t)key * a.C + c, acc);

@@ -15,6 +15,10 @@ SHAPES = [(1, 0, 1), (1, 0, 16), (64, 2, 16), (5, 4, 16), (7, 1, 20), (3, 3, 31)
           (23, 2, 200), (700, 1, 256), (6, 4, 252), (10, 4, 255), (4, 4, 256), (4, 2, 260), (19, 0, 257),
           (30, 0, 1000), (5, 1, 1001), (7, 0, 4096), (3, 0, 8190), (2, 0, 16384), (2, 4, 1024), (2, 0, 16381)]
 
+# enough nodes that every warp takes several units, at each degree's layout
+LONG = [(6000, 4, 128), (9000, 2, 64), (3000, 4, 256), (20000, 1, 16), (5000, 3, 36), (6000, 2, 101), (3000, 1, 255),
+        (5000, 0, 1001), (1500, 0, 5001), (30000, 0, 33), (3000, 0, 2048), (700, 0, 8190), (400, 1, 300)]
+
 
 def _x(n, L, C, dtype, seed=0, offset=0.5):
     g = torch.Generator().manual_seed(seed)
@@ -106,6 +110,33 @@ def test_backward(n, L, C, xt):
     assert torch.equal(at, g["x"])
 
 
+@pytest.mark.parametrize("xt", ["f32", "bf16", "mxi8"])
+@pytest.mark.parametrize("n,L,C", LONG)
+def test_long_batches(n, L, C, xt):
+    """Forward with the residual and the checkpoint where x is no checkpoint, and backward. The weight gradient's
+    longest chain is still below 1024: a lane's rows of its units, then the block's lanes, then the blocks."""
+    x, w, b, r = _x(n, L, C, "f32" if xt == "mxi8" else xt, seed=n + C + 4)
+    gy = torch.randn(x.shape, generator=torch.Generator().manual_seed(6))
+    cfg = e2f.make_norm_cfg(L, C, xt, "bf16", EPS)
+    if xt == "mxi8":
+        h, code, byte = R.coded(x)
+        dev, scales = code.cuda(), byte.cuda()
+        f = e2f.e2f_layer_norm(cfg, dev, w.cuda(), b.cuda(), x_scales=scales)
+    else:
+        f = e2f.e2f_layer_norm(cfg, x.cuda(), w.cuda(), b.cuda(), residual=r.cuda(), checkpoint=True)
+        h, scales, dev = (x.float() + r).to(x.dtype), None, f["sum"]
+        assert torch.equal(dev.cpu(), h)
+        _, code, byte = R.coded(h)
+        assert torch.equal(f["codes"].cpu(), code) and torch.equal(f["scales"].cpu(), byte)
+        h = h.double()
+    _check_forward((xt, "bf16"), f, h, w, b, L)
+    mean, rstd = f["mean"].cpu().double(), f["rstd"].cpu().double()
+    g = e2f.e2f_layer_norm_backward(cfg, dev, w.cuda(), f["mean"], f["rstd"], gy.cuda(), x_scales=scales)
+    ref = (h, w.double(), mean, rstd, gy.double(), L)
+    for name, want, bound in zip(("x", "weight", "bias"), R.norm_backward(*ref), R.norm_backward_bound(*ref)):
+        _within(g[name], want, bound, name)
+
+
 @pytest.mark.parametrize("n,L,C", [(9, 4, 128), (20, 0, 1000), (6, 2, 33)])
 def test_gradient_against_differences(n, L, C):
     """The kernel's gradients along a random direction against a central difference of the 64-bit forward (which
@@ -185,9 +216,10 @@ def test_only_the_given_rows_are_written(n, L, C):
     assert (gx[n:] == 77).all()
 
 
-def test_the_residual_stream_in_place():
-    x, w, b, r = _x(64, 4, 128, "bf16")
-    cfg = e2f.make_norm_cfg(4, 128, "bf16", "bf16", EPS)
+@pytest.mark.parametrize("n,L,C", [(64, 4, 128), (2000, 3, 100), (500, 2, 101), (300, 0, 1001), (90, 0, 4096), (40, 1, 300)])
+def test_the_residual_stream_in_place(n, L, C):
+    x, w, b, r = _x(n, L, C, "bf16")
+    cfg = e2f.make_norm_cfg(L, C, "bf16", "bf16", EPS)
     want = e2f.e2f_layer_norm(cfg, x.cuda(), w.cuda(), b.cuda(), residual=r.cuda(), checkpoint=True)
     at = x.cuda()
     got = e2f.e2f_layer_norm(cfg, at, w.cuda(), b.cuda(), residual=r.cuda(), checkpoint=True, out={"sum": at})
