@@ -109,6 +109,11 @@ __device__ __forceinline__ float mag_max(float a, float b) {
     return r;
 }
 
+// the unit 2^(s - 133) of a block, exact (at least 2^-133)
+__device__ __forceinline__ float ck_unit(uint32_t s) {
+    return s - 7u <= 247u ? __uint_as_float((s - 6u) << 23) : ck_scale(s) * 0.015625f;
+}
+
 // code of v in a block of scale byte s < 255: rint(v 2^(6-e)) clamped to +-127,
 // in the low byte. The scaling is a power of two and fma rounds once, to whole
 // numbers at 1.5 2^23 (half to even): the code does not depend on how it is computed.
@@ -138,7 +143,10 @@ struct Raw4;
 template <>
 struct Raw4<kF32> {
     float4 a;
-    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const float4*>(p); }
+    // from shared memory, by its 32-bit address
+    __device__ __forceinline__ void from(uint32_t p) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "r"(p));
+    }
     __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
         a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
     }
@@ -149,7 +157,9 @@ struct Raw4<kF32> {
 template <>
 struct Raw4<kBF16> {
     uint2 a;
-    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const uint2*>(p); }
+    __device__ __forceinline__ void from(uint32_t p) {
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a.x), "=r"(a.y) : "r"(p));
+    }
     __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
         a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
@@ -161,13 +171,13 @@ struct Raw4<kBF16> {
 template <>
 struct Raw4<kMXI8> {
     uint32_t a, s;
-    __device__ __forceinline__ void from(const void* p) { a = *static_cast<const uint32_t*>(p); }
+    __device__ __forceinline__ void from(uint32_t p) { asm volatile("ld.shared.u32 %0, [%1];" : "=r"(a) : "r"(p)); }
     __device__ __forceinline__ void load(const void* p, const uint8_t* scales, int64_t i, int64_t block) {
         a = *reinterpret_cast<const uint32_t*>(static_cast<const int8_t*>(p) + i);
         s = scales[block];
     }
     __device__ __forceinline__ void get(float (&v)[4]) const {
-        const float u = ck_scale(s) * 0.015625f;  // exact: at least 2^-133
+        const float u = ck_unit(s);
         const uint32_t b = a ^ 0x80808080u;
         v[0] = ck_value(b, 0x7650) * u; v[1] = ck_value(b, 0x7651) * u;
         v[2] = ck_value(b, 0x7652) * u; v[3] = ck_value(b, 0x7653) * u;
@@ -183,7 +193,7 @@ __device__ __forceinline__ void load_codes(const int8_t* codes, const uint8_t* s
         r.load(codes, scales, row * C + c, row * nb + c / kCkBlock);
         r.get(v);
     } else {
-        const float u = ck_scale(scales[row * nb + c / kCkBlock]) * 0.015625f;
+        const float u = ck_unit(scales[row * nb + c / kCkBlock]);
         for (int k = 0; k < V; ++k) v[k] = codes[row * C + c + k] * u;
     }
 }

@@ -13,9 +13,9 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
     constexpr int V = 4, E = vec_bytes<XT>() / 4, R = U::R, B = U::B;  // E: bytes of a value
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, t = lane & (TL - 1), C = a.C;
     const int K = (a.L + 1) * (a.L + 1), teams = 32 / TL, team0 = lane / TL * (B * R);
-    const char* zeros = smem + warps * sl.stages * sl.stage_bytes;  // what lanes beyond the row read
-    const char* mine = smem + warp * sl.stages * sl.stage_bytes;
-    const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint32_t smem_s = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint32_t zeros = smem_s + warps * sl.stages * sl.stage_bytes;  // what lanes beyond the row read
+    const uint32_t mine_s = smem_s + warp * sl.stages * sl.stage_bytes;
     int c[NI];
     bool in[NI];
     float w[NI][V], bias[NI][V] = {};
@@ -38,28 +38,21 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
         }
         cp_commit();
     };
-    uint32_t scale[B * R][NI] = {}, next[B * R][NI] = {};  // of the unit in work and of the next one, where x has any
-    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+    uint32_t scale[B * R][NI] = {};  // of the next unit, where x has any
+    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, scale);
     for (int s = 0; s + 1 < sl.stages; ++s) fetch(k + s * step, s);
     for (int s = 0; k < units; k += step, s = s + 1 == sl.stages ? 0 : s + 1) {
         const U u(k, a.n, K, TL);
         __syncwarp();  // the whole warp is done with the stage that is filled next
         fetch(k + (sl.stages - 1) * step, s == 0 ? sl.stages - 1 : s - 1);
-        if constexpr (XT == kMXI8) {
-#pragma unroll
-            for (int m = 0; m < B * R; ++m)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) scale[m][i] = next[m][i];
-            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
-        }
         cp_wait(sl.stages - 1);
         __syncwarp();
-        const char* st = mine + s * sl.stage_bytes;
+        const uint32_t st = mine_s + s * sl.stage_bytes;
         const int64_t base = u.row0 * C;
         float v[B][R][NI][V];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const char* p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
+            const uint32_t p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
             const int pitch = in[i] ? C * E : 0;
 #pragma unroll
             for (int b = 0; b < B; ++b)
@@ -72,16 +65,17 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
                 }
             if constexpr (XT != kMXI8) {
                 if (a.res) {
-                    const char* r = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
+                    const uint32_t r = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
                     const int r_pitch = in[i] ? C * 4 : 0;
 #pragma unroll
                     for (int b = 0; b < B; ++b)
 #pragma unroll
                         for (int m = 0; m < R; ++m) {
-                            const float4 e = *reinterpret_cast<const float4*>(r + (b * R + m) * r_pitch);
+                            Raw4<kF32> e;
+                            e.from(r + (b * R + m) * r_pitch);
                             float (&h)[V] = v[b][m][i];
-                            h[0] = as_stored<XT>(h[0] + e.x); h[1] = as_stored<XT>(h[1] + e.y);
-                            h[2] = as_stored<XT>(h[2] + e.z); h[3] = as_stored<XT>(h[3] + e.w);
+                            h[0] = as_stored<XT>(h[0] + e.a.x); h[1] = as_stored<XT>(h[1] + e.a.y);
+                            h[2] = as_stored<XT>(h[2] + e.a.z); h[3] = as_stored<XT>(h[3] + e.a.w);
                             if (b < u.have && in[i])
                                 store_vec<XT, V>(a.sum, base + ((b * teams * K + m) * C + c[i]), h);
                         }
@@ -95,6 +89,8 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
                                            b < u.have && in[i], TL, v[b][m][i]);
             }
         }
+        if constexpr (XT == kMXI8)
+            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, scale);
         float mu[B], q[B];
         if constexpr (l == 0) {
 #pragma unroll

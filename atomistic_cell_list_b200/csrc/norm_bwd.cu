@@ -18,9 +18,9 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
     constexpr int V = 4, E = vec_bytes<XT>() / 4, R = U::R, B = U::B;
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5, lane = threadIdx.x & 31, t = lane & (TL - 1), C = a.C;
     const int K = (a.L + 1) * (a.L + 1), teams = 32 / TL, team = lane / TL, team0 = team * (B * R);
-    const char* zeros = smem + warps * sl.stages * sl.stage_bytes;
-    const char* mine = smem + warp * sl.stages * sl.stage_bytes;
-    const uint32_t mine_s = (uint32_t)__cvta_generic_to_shared(mine);
+    const uint32_t smem_s = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint32_t zeros = smem_s + warps * sl.stages * sl.stage_bytes;
+    const uint32_t mine_s = smem_s + warp * sl.stages * sl.stage_bytes;
     int c[NI];
     bool in[NI];
     float w[NI][V], dw[NI][V] = {}, db[NI][V] = {};
@@ -49,24 +49,17 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
         }
         cp_commit();
     };
-    uint32_t scale[B * R][NI] = {}, next[B * R][NI] = {};
-    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
+    uint32_t scale[B * R][NI] = {};  // of the next unit, where x has any
+    if (XT == kMXI8 && k < units) U(k, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, scale);
     for (int s = 0; s + 1 < sl.stages; ++s) fetch(k + s * step, s);
     for (int s = 0; k < units; k += step, s = s + 1 == sl.stages ? 0 : s + 1) {
         const U u(k, a.n, K, TL);
         __syncwarp();  // the whole warp is done with the stage that is filled next
         fetch(k + (sl.stages - 1) * step, s == 0 ? sl.stages - 1 : s - 1);
-        if constexpr (XT == kMXI8) {
-#pragma unroll
-            for (int m = 0; m < B * R; ++m)
-#pragma unroll
-                for (int i = 0; i < NI; ++i) scale[m][i] = next[m][i];
-            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, next);
-        }
         cp_wait(sl.stages - 1);
         __syncwarp();
-        const char* st = mine + s * sl.stage_bytes;
-        const float* stat = reinterpret_cast<const float*>(st + sl.o3) + team * B;
+        const uint32_t st = mine_s + s * sl.stage_bytes;
+        const float* stat = reinterpret_cast<const float*>(smem + (st - smem_s) + sl.o3) + team * B;
         float x[B][R][NI][V], g[B][R][NI][V], r[B], s1[B], s2[B];  // x becomes xh, g becomes u = grad_y weight
 #pragma unroll
         for (int b = 0; b < B; ++b) {
@@ -76,8 +69,8 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
             const bool ok = b < u.have;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const char* p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
-                const char* pg = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
+                const uint32_t p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
+                const uint32_t pg = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
                 const int pitch = in[i] ? C : 0;
 #pragma unroll
                 for (int m = 0; m < R; ++m) {
@@ -86,8 +79,9 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                     raw.from(p + (b * R + m) * pitch * E);
                     if constexpr (XT == kMXI8) raw.s = scale[b * R + m][i];
                     raw.get(xv);
-                    const float4 e = *reinterpret_cast<const float4*>(pg + (b * R + m) * pitch * 4);
-                    const float gv[V] = {e.x, e.y, e.z, e.w};
+                    Raw4<kF32> e;
+                    e.from(pg + (b * R + m) * pitch * 4);
+                    const float gv[V] = {e.a.x, e.a.y, e.a.z, e.a.w};
                     for (int k = 0; k < V; ++k) {
                         const float xh = (l == 0 ? xv[k] - mu : xv[k]) * r[b], uk = gv[k] * w[i][k];
                         if (ok) dw[i][k] += gv[k] * xh;
@@ -102,6 +96,8 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                 }
             }
         }
+        if constexpr (XT == kMXI8)
+            if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, scale);
         if constexpr (l == 0) team_sum(s1, TL);
         team_sum(s2, TL);
         const int64_t base = u.row0 * C;
@@ -117,9 +113,9 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                         for (int k = 0; k < V; ++k)
                             o[k] = fmaf(-x[b][m][i][k], m2, l == 0 ? fmaf(r[b], g[b][m][i][k], -m1) : r[b] * g[b][m][i][k]);
                         if (a.skip) {
-                            const float4 e = *reinterpret_cast<const float4*>(
-                                st + sl.o2 + ((team0 + b * R + m) * C + c[i]) * 4);
-                            o[0] += e.x; o[1] += e.y; o[2] += e.z; o[3] += e.w;
+                            Raw4<kF32> e;
+                            e.from(st + sl.o2 + ((team0 + b * R + m) * C + c[i]) * 4);
+                            o[0] += e.a.x; o[1] += e.a.y; o[2] += e.a.z; o[3] += e.a.w;
                         }
                         store_vec<kF32, V>(a.gx, base + ((b * teams * K + m) * C + c[i]), o);
                     }
