@@ -1,6 +1,7 @@
-"""Python binding of libe2f.so: a GPU cell-list neighbour build and the
-on-the-fly equivariant attention forward of E2Former-V2, written for B200
-(sm_100a).
+"""Python binding of libe2f.so: a GPU cell-list neighbour build, the
+on-the-fly equivariant attention of E2Former-V2 with its gradients, and the
+operators around it (norm, 8-bit checkpoints, species embedding), written
+for B200 (sm_100a).
 
 This module only marshals arguments: every step of the computation runs in
 the library's CUDA kernels. PyTorch supplies device memory and the current
@@ -607,7 +608,8 @@ def make_embed_cfg(n_tokens: int, C: int, L: int = 0, scale: float = 1.0, table_
 def e2f_embedding(cfg: e2f_embed_cfg, tokens, table, out: torch.Tensor | None = None, stream=None,
                   check: bool = True) -> torch.Tensor:
     """out[N, (L+1)^2, C]: scaled table rows of int32 tokens as degree-0 features (see include/e2f.h). Negative
-    tokens are padding. With check, a token beyond the table raises E2FError (this waits for the stream)."""
+    tokens are padding. With check, a token beyond the table raises E2FError; this waits for the stream, so a
+    call that is captured into a graph passes check=False."""
     n, dev = tokens.shape[0] if tokens.dim() else 0, tokens.device
     pt = _operand("tokens", tokens, torch.int32, (n,))
     pw = _operand("table", table, _TORCH[cfg.table_dtype], (cfg.n_tokens, cfg.C), dev)

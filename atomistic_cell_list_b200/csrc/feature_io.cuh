@@ -147,9 +147,6 @@ struct Raw4<kF32> {
     __device__ __forceinline__ void from(uint32_t p) {
         asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(a.x), "=f"(a.y), "=f"(a.z), "=f"(a.w) : "r"(p));
     }
-    __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
-        a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-    }
     __device__ __forceinline__ void get(float (&v)[4]) const {
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     }
@@ -159,9 +156,6 @@ struct Raw4<kBF16> {
     uint2 a;
     __device__ __forceinline__ void from(uint32_t p) {
         asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(a.x), "=r"(a.y) : "r"(p));
-    }
-    __device__ __forceinline__ void load(const void* p, const uint8_t*, int64_t i, int64_t) {
-        a = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + i);
     }
     __device__ __forceinline__ void get(float (&v)[4]) const {
         v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);

@@ -6,7 +6,10 @@ namespace {
 
 constexpr int kFwdWarps = 8;  // of a block, at 128 registers
 
-// the units of degree l that this block takes
+// The units of degree l that this block takes. 3,000 atoms, L = 4, C = 128, fp32
+// stream + fp32 residual -> stream and bf16 features: 134 MB in 24 us (5.6 TB/s).
+// 20,000 atoms with the checkpoint beside them: 0.96 GB in 170 us. From codes to bf16
+// (194 MB in 73 us) it is bound by instructions, 83 per row of 128 values.
 template <int XT, int YT, int NI, int l>
 __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slots& sl, char* smem) {
     using U = Unit<NI, l>;
@@ -158,7 +161,8 @@ __global__ void __launch_bounds__(32 * kFwdWarps, 2) k_norm_teams(NormArgs a, in
     else norm_degree<XT, YT, NI, 4>(a, TL, sl, smem);
 }
 
-// One block per (node, degree); any C.
+// One block per (node, degree), for L >= 1 with more than 256 channels: reads its
+// group once per pass, from the second on out of L2.
 template <int XT, int YT, int V>
 __global__ void k_norm_rows(NormArgs a) {
     __shared__ float sh[32];
@@ -219,8 +223,10 @@ __global__ void k_norm_rows(NormArgs a) {
 
 // L = 0: one block per row, the row in registers, NV vectors of V values a thread.
 // All of a row's loads are in flight together; rows of other blocks of the SM hide
-// the two sums. TT > 0: that many threads, so that the offsets of a thread's values
-// are constants (value by value, the instructions bound it: 55 a value became 20).
+// the two sums. 8,192 rows of 4,096 fp32 values with a residual, 470 MB in 71 us (the
+// copy rate). TT > 0: that many threads, so that the offsets of a thread's values are
+// constants; where V = 1 the instructions bound it (20,000 rows of 1,001 fp32 values:
+// 47 us without, 31 us with; 4,099 rows of 5,001 bf16 values: 42 us, 2 TB/s).
 template <int XT, int YT, int V, int NV, int TT>
 __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_held(NormArgs a) {
     __shared__ float sh[32];

@@ -1,8 +1,8 @@
 // Layer norm of irreducible features for up to 256 channels that are no multiple of 4: rows begin on any 4 (fp32),
 // 2 (bf16) or 1 (codes) bytes, so values are loaded one by one. One warp per unit of up to 9 rows, a lane owns the
 // channels lane + 32 i, i < NI, and holds them for all rows of the unit; blocks work on one degree (norm.cuh). All
-// loads of a unit are in flight together. fp32 moves 128 bytes an instruction: 20,000 atoms, L = 4, C = 101 run at
-// about the speed of C = 100 with its 16-byte pieces; what bounds it are instructions.
+// loads of a unit are in flight together. fp32 moves 128 bytes an instruction; instructions bound it: 20,000 atoms,
+// L = 4, C = 101 take 85 us forward and 221 us backward, C = 100 with its 16-byte pieces 62 and 118 us.
 #include "norm.cuh"
 
 namespace e2f {
