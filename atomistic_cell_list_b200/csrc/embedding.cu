@@ -5,8 +5,8 @@
 // T tokens; teams of lanes sum equal parts of the tile, run by run; the runs that
 // cross parts are added in the block, those that cross tiles by a second kernel.
 //   Tables of up to 256 rows (species): each tile is sorted by itself, in shared
-//   memory. A block's sums of its distinct tokens are at most half of what it
-//   reads, and two launches do it all (one for a single tile).
+//   memory. A block writes a sum for each of its distinct tokens, and two launches
+//   do it all (one for a single tile).
 //   100,000 tokens of two species, C = 128: 51 MB in 20 us, 63 us with a global sort and
 //   a join of 64-token chunks; latency bounds it (the sort of a tile, its rows 8 at a time).
 //   Larger tables: a stable radix sort of all tokens first, 8 bits a pass. 65,536

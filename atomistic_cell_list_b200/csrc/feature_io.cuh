@@ -206,9 +206,10 @@ __device__ __forceinline__ void load_feat(const void* p, const uint8_t* s, int64
 // Checkpoint of V channels per lane, lanes in channel order: a block of 32
 // channels is 32/V lanes, fewer when the lanes of a row (`team`) are fewer.
 // Every lane of the warp calls it; lanes beyond the row pass zeros and ok = false.
+// at: where this lane's codes go; scale: where its block's byte goes, written by the block's first lane.
 template <int V>
-__device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int64_t row, int C, int nb, int c, bool ok,
-                                            int team, const float (&v)[V]) {
+__device__ __forceinline__ void store_codes_at(int8_t* at, uint8_t* scale, bool first, bool ok, int team,
+                                               const float (&v)[V]) {
     float m = fabsf(v[0]);
     for (int k = 1; k < V; ++k) m = mag_max(m, v[k]);
     constexpr int G = kCkBlock / V;
@@ -217,13 +218,18 @@ __device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int6
     if (!ok) return;
     const uint32_t s = ck_byte(m);
     const float inv = ck_inverse(s);
-    int8_t* q = codes + row * C + c;
     if constexpr (V == 4) {
-        *reinterpret_cast<uint32_t*>(q) = s == 255u ? 0u : pack_codes(v[0], v[1], v[2], v[3], inv);
+        *reinterpret_cast<uint32_t*>(at) = s == 255u ? 0u : pack_codes(v[0], v[1], v[2], v[3], inv);
     } else {
-        for (int k = 0; k < V; ++k) q[k] = s == 255u ? 0 : (int8_t)ck_code(v[k], inv);
+        for (int k = 0; k < V; ++k) at[k] = s == 255u ? 0 : (int8_t)ck_code(v[k], inv);
     }
-    if (c % kCkBlock == 0) scales[row * nb + c / kCkBlock] = (uint8_t)s;
+    if (first) *scale = (uint8_t)s;
+}
+
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t* codes, uint8_t* scales, int64_t row, int C, int nb, int c, bool ok,
+                                            int team, const float (&v)[V]) {
+    store_codes_at<V>(codes + row * C + c, scales + row * nb + c / kCkBlock, c % kCkBlock == 0, ok, team, v);
 }
 
 }  // namespace e2f

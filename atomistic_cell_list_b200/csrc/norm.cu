@@ -51,7 +51,9 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
         cp_wait(sl.stages - 1);
         __syncwarp();
         const uint32_t st = mine_s + s * sl.stage_bytes;
+        // addresses run along with the rows: a node's rows follow one another, the team's nodes lie jump rows apart
         const int64_t base = u.row0 * C;
+        const int jump = teams * K;
         float v[B][R][NI][V];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
@@ -70,8 +72,10 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
                 if (a.res) {
                     const uint32_t r = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
                     const int r_pitch = in[i] ? C * 4 : 0;
+                    char* sum = static_cast<char*>(a.sum) + (base + c[i]) * E;
 #pragma unroll
-                    for (int b = 0; b < B; ++b)
+                    for (int b = 0; b < B; ++b) {
+                        char* to = sum;
 #pragma unroll
                         for (int m = 0; m < R; ++m) {
                             Raw4<kF32> e;
@@ -79,17 +83,29 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
                             float (&h)[V] = v[b][m][i];
                             h[0] = as_stored<XT>(h[0] + e.a.x); h[1] = as_stored<XT>(h[1] + e.a.y);
                             h[2] = as_stored<XT>(h[2] + e.a.z); h[3] = as_stored<XT>(h[3] + e.a.w);
-                            if (b < u.have && in[i])
-                                store_vec<XT, V>(a.sum, base + ((b * teams * K + m) * C + c[i]), h);
+                            if (b < u.have && in[i]) store_vec<XT, V>(to, 0, h);
+                            to += C * E;
                         }
+                        sum += (int64_t)jump * C * E;
+                    }
                 }
-                if (a.codes)
+                if (a.codes) {
+                    int8_t* codes = a.codes + base + c[i];
+                    uint8_t* scales = a.scales + u.row0 * a.nb + c[i] / kCkBlock;
 #pragma unroll
-                    for (int b = 0; b < B; ++b)
+                    for (int b = 0; b < B; ++b) {
+                        int8_t* to = codes;
+                        uint8_t* to_s = scales;
 #pragma unroll
-                        for (int m = 0; m < R; ++m)
-                            store_codes<V>(a.codes, a.scales, u.row0 + (b * teams * K + m), C, a.nb, c[i],
-                                           b < u.have && in[i], TL, v[b][m][i]);
+                        for (int m = 0; m < R; ++m) {
+                            store_codes_at<V>(to, to_s, c[i] % kCkBlock == 0, b < u.have && in[i], TL, v[b][m][i]);
+                            to += C;
+                            to_s += a.nb;
+                        }
+                        codes += (int64_t)jump * C;
+                        scales += (int64_t)jump * a.nb;
+                    }
+                }
             }
         }
         if constexpr (XT == kMXI8)
@@ -129,13 +145,16 @@ __device__ __forceinline__ void norm_degree(const NormArgs& a, int TL, const Slo
             for (int i = 0; i < NI; ++i) {
                 float f[V];
                 for (int k = 0; k < V; ++k) f[k] = q[b] * w[i][k];
+                constexpr int EY = vec_bytes<YT>() / 4;
+                char* to = static_cast<char*>(a.y) + (base + (int64_t)(b * jump) * C + c[i]) * EY;
                 if (b < u.have && in[i])
 #pragma unroll
                     for (int m = 0; m < R; ++m) {
                         float y[V];
                         for (int k = 0; k < V; ++k)
                             y[k] = l == 0 ? fmaf(v[b][m][i][k], f[k], bias[i][k]) : v[b][m][i][k] * f[k];
-                        store_vec<YT, V>(a.y, base + ((b * teams * K + m) * C + c[i]), y);
+                        store_vec<YT, V>(to, 0, y);
+                        to += C * EY;
                     }
             }
             if (t == 0 && b < u.have) {

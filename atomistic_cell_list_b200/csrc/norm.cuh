@@ -196,14 +196,18 @@ struct Unit {
     // scale bytes of a checkpoint's vectors, one lane's
     __device__ __forceinline__ void scales(const uint8_t* xs, int nb, int K, int TL, const int (&c)[NI],
                                            uint32_t (&s)[B * R][NI]) const {
-        const uint8_t* q = xs + row0 * nb;
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (b < have)
+        for (int i = 0; i < NI; ++i) {
+            const uint8_t* q = xs + row0 * nb + c[i] / kCkBlock;
 #pragma unroll
-                for (int m = 0; m < R; ++m)
+            for (int b = 0; b < B; ++b) {
+                const uint8_t* p = q;
+                if (b < have)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) s[b * R + m][i] = q[(b * (32 / TL * K) + m) * nb + c[i] / kCkBlock];
+                    for (int m = 0; m < R; ++m, p += nb) s[b * R + m][i] = *p;
+                q += (int64_t)(32 / TL * K) * nb;
+            }
+        }
     }
 };
 

@@ -108,7 +108,8 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
         for (int b = 0; b < B; ++b) {
             const float m1 = s1[b] * a.inv_c * r[b], m2 = s2[b] * (a.inv_c * (1.f / R)) * r[b];
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
+            for (int i = 0; i < NI; ++i) {
+                float* to = a.gx + base + (int64_t)(b * teams * K) * C + c[i];
                 if (b < u.have && in[i])
 #pragma unroll
                     for (int m = 0; m < R; ++m) {
@@ -120,8 +121,10 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                             e.from(st + sl.o2 + ((team0 + b * R + m) * C + c[i]) * 4);
                             o[0] += e.a.x; o[1] += e.a.y; o[2] += e.a.z; o[3] += e.a.w;
                         }
-                        store_vec<kF32, V>(a.gx, base + ((b * teams * K + m) * C + c[i]), o);
+                        store_vec<kF32, V>(to, 0, o);
+                        to += C;
                     }
+            }
         }
     }
     if (!a.part) return;
