@@ -287,7 +287,7 @@ __device__ __forceinline__ bool sort_tile(const int32_t* tok, int64_t base, int 
         }
         __syncthreads();
         if (sweep == 0) {
-            // token k's places: smaller tokens, then the warps before (thread k, and the last key by thread 0)
+            // token k's places: smaller tokens, then the warps before (thread k; key 256 by thread 255)
             __shared__ uint32_t ws[8];
             uint32_t all = 0;
             for (int q = 0; q < 8; ++q) all += wc[q][threadIdx.x];

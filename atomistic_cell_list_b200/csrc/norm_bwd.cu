@@ -231,9 +231,10 @@ __global__ void k_norm_bwd_rows(NormBwdArgs a) {
 
 // L = 0: persistent blocks, one row at a time in registers, NV vectors of V values
 // of x and of grad_y a thread, with the weight and bias gradient of its channels:
-// each value is read once. 8,192 rows of 4,096 fp32 values with a skip gradient:
-// 537 MB in 113 us; what bounds it are the two sums of a row, which the one or two
-// resident blocks do not hide. 20,000 rows of 1,001, value by value: 54 us.
+// each value is read once, and a row's loads are issued before the sums of the row
+// before it. 8,192 rows of 4,096 fp32 values with a skip gradient: 537 MB in 101 us
+// (5.3 TB/s; 113 us without the early loads). 20,000 rows of 1,001, value by value:
+// 54 us; 4,096 rows of 5,001 with bf16 x: 85 us, bound by instructions.
 // part: [block][C], then [block][C] for the bias.
 template <int XT, int V, int NV, int TT>
 __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a) {
@@ -241,13 +242,13 @@ __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a)
     const int T = TT ? TT : blockDim.x, C = a.C - threadIdx.x * V;  // this thread's vector j exists: j T V < C
     float dw[NV][V] = {}, db[NV][V] = {};
     const float* wp = a.w + threadIdx.x * V;
-    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    float x[NV][V], g[NV][V], mu = 0.f, r = 0.f;
+    auto load = [&](int64_t row, float (&x)[NV][V], float (&g)[NV][V], float& mu, float& r) {
         const int64_t base = row * a.C + threadIdx.x * V;
         const char* xp = static_cast<const char*>(a.x) + base * (vec_bytes<XT>() / 4);
-        const float *gp = a.gy + base, *kp = a.skip + base;
-        float* op = a.gx + base;
-        float x[NV][V], g[NV][V], s1 = 0.f, s2 = 0.f;
-        const float mu = a.mean[row], r = a.rstd[row];
+        const float* gp = a.gy + base;
+        mu = a.mean[row];
+        r = a.rstd[row];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             for (int k = 0; k < V; ++k) x[j][k] = g[j][k] = 0.f;
@@ -259,6 +260,13 @@ __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a)
                 load_vec<kF32, V>(gp, j * T * V, g[j]);
             }
         }
+    };
+    if (blockIdx.x < a.n) load(blockIdx.x, x, g, mu, r);
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C + threadIdx.x * V;
+        const float* kp = a.skip + base;
+        float* op = a.gx + base;
+        float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (j * T * V < C) {
@@ -274,6 +282,9 @@ __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a)
                     g[j][k] = u;
                 }
             }
+        // the next row is on its way while this one's sums are formed
+        float xn[NV][V], gn[NV][V], mun = 0.f, rn = 0.f;
+        if (row + gridDim.x < a.n) load(row + gridDim.x, xn, gn, mun, rn);
         const float m1 = block_sum(s1, sh[0]) * a.inv_c, m2 = block_sum(s2, sh[1]) * a.inv_c;
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -283,6 +294,14 @@ __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a)
                 for (int k = 0; k < V; ++k) e[k] += r * (g[j][k] - m1 - x[j][k] * m2);
                 store_vec<kF32, V>(op, j * T * V, e);
             }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            for (int k = 0; k < V; ++k) {
+                x[j][k] = xn[j][k];
+                g[j][k] = gn[j][k];
+            }
+        mu = mun;
+        r = rn;
     }
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * a.C + threadIdx.x * V;
@@ -352,10 +371,10 @@ int bwd_held(int L, int C) {
     return C <= 1024 ? 128 : C <= 6144 ? 512 : 0;
 }
 
-// blocks of k_norm_bwd_held (about 1,024 threads an SM: more partials would cost
-// more than they hide), or blocks per row of features of k_norm_bwd_rows
+// blocks of k_norm_bwd_held (at most 1,024 threads and 5 blocks an SM, what fits at
+// once by registers: a second wave costs more than it hides), or blocks per row of features of k_norm_bwd_rows
 int rows_blocks(int64_t n, int L, int C) {
-    const int t = bwd_held(L, C), most = t ? kSMs * std::max(1, std::min(8, 1024 / t)) : kNormBlocks / ((L + 1) * (L + 1));
+    const int t = bwd_held(L, C), most = t ? kSMs * std::max(1, std::min(5, 1024 / t)) : kNormBlocks / ((L + 1) * (L + 1));
     return (int)std::max<int64_t>(1, std::min<int64_t>(n, most));
 }
 
