@@ -244,8 +244,9 @@ __global__ void k_norm_rows(NormArgs a) {
 // All of a row's loads are in flight together; rows of other blocks of the SM hide
 // the two sums. 8,192 rows of 4,096 fp32 values with a residual, 470 MB in 71 us (the
 // copy rate). TT > 0: that many threads, so that the offsets of a thread's values are
-// constants; where V = 1 the instructions bound it (20,000 rows of 1,001 fp32 values:
-// 47 us without, 31 us with; 4,099 rows of 5,001 bf16 values: 42 us, 2 TB/s).
+// constants; where V = 1 the instructions bound it (4,099 rows of 5,001 bf16 values:
+// 42 us, 46 us without). V = 1 serves codes, rows with a checkpoint and the longest rows;
+// the others run in k_norm_kept.
 template <int XT, int YT, int V, int NV, int TT>
 __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_held(NormArgs a) {
     __shared__ float sh[32];
@@ -316,6 +317,91 @@ __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_held(NormArgs a) {
     }
 }
 
+// A value as storage keeps it, so that its load can be under way while the one before it is in use.
+template <int T>
+struct Raw1 {
+    float a;
+    __device__ __forceinline__ void load(const char* p, int i) { a = reinterpret_cast<const float*>(p)[i]; }
+    __device__ __forceinline__ float get() const { return a; }
+};
+template <>
+struct Raw1<kBF16> {
+    unsigned short a;
+    __device__ __forceinline__ void load(const char* p, int i) { a = reinterpret_cast<const unsigned short*>(p)[i]; }
+    __device__ __forceinline__ float get() const { return __uint_as_float((uint32_t)a << 16); }
+};
+
+// L = 0, fp32 or bf16 rows that no vector divides: persistent blocks, a thread's
+// weights in registers from row to row, the next row's values under way while this
+// one's sums are formed. Instructions bound it (one load, one store and about ten
+// more a value). 4,099 rows of 5,001 bf16 values: 30 us (2.8 TB/s; one block per row
+// 42 us), at 384 threads of 16 values (1,024 of 8: 37 us); 4,096 rows of 8,190: 43 us
+// at 1,024 threads of 8 (512 of 16: 66 us); 20,000 rows of 1,001 fp32 values: 28 us
+// (5.7 TB/s).
+template <int XT, int YT, int NV, int TT>
+__global__ void __launch_bounds__(TT) k_norm_kept(NormArgs a) {
+    constexpr int E = vec_bytes<XT>() / 4, EY = vec_bytes<YT>() / 4;
+    __shared__ float sh[2][32];
+    const int C = a.C - threadIdx.x;  // this thread's value j exists: j TT < C
+    float w[NV], b[NV];
+    Raw1<XT> next[NV];
+    auto load = [&](int64_t row) {
+        const char* x = static_cast<const char*>(a.x) + (row * a.C + threadIdx.x) * E;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (j * TT < C) next[j].load(x, j * TT);
+    };
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        w[j] = j * TT < C ? a.w[threadIdx.x + j * TT] : 0.f;
+        b[j] = j * TT < C && a.b ? a.b[threadIdx.x + j * TT] : 0.f;
+        next[j].a = 0;
+    }
+    if (blockIdx.x < a.n) load(blockIdx.x);
+    for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+        const int64_t base = row * a.C + threadIdx.x;
+        float v[NV], s = 0.f, q = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) v[j] = next[j].get();
+        if (a.res)
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (j * TT < C) {
+                    const float h[1] = {as_stored<XT>(v[j] + a.res[base + j * TT])};
+                    v[j] = h[0];
+                    store_vec<XT, 1>(static_cast<char*>(a.sum) + base * E, j * TT, h);
+                }
+        if (row + gridDim.x < a.n) load(row + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < NV; ++j) s += v[j];  // values beyond the row are zero
+        const float mu = block_sum(s, sh[0]) * a.inv_c;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            v[j] -= mu;
+            if (j * TT < C) q = fmaf(v[j], v[j], q);
+        }
+        const float r = rsqrtf(block_sum(q, sh[1]) * a.inv_c + a.eps);
+        char* y = static_cast<char*>(a.y) + base * EY;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const float o[1] = {fmaf(v[j] * r, w[j], b[j])};
+            if (j * TT < C) store_vec<YT, 1>(y, j * TT, o);
+        }
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mu;
+            if (a.rstd) a.rstd[row] = r;
+        }
+    }
+}
+
+template <int XT, int YT, int NV, int TT>
+cudaError_t launch_kept(const NormArgs& a, cudaStream_t s) {
+    // the blocks that fit at once: 64 registers a thread at NV = 8, about 80 at 16
+    constexpr int per_sm = (NV == 8 ? 1024 : 768) / TT;
+    k_norm_kept<XT, YT, NV, TT><<<(unsigned)std::min<int64_t>(a.n, kSMs * per_sm), TT, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int XT, int YT, int NI>
 cudaError_t launch_teams(const NormArgs& a, const TeamPlan& p, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(k_norm_teams<XT, YT, NI>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBlockSmem);
@@ -338,7 +424,13 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t s) {
     if (a.L == 0) {  // C <= 16384 always fits
         const unsigned grid = (unsigned)a.n;
         if (a.C % 4 == 0) k_norm_held<XT, YT, 4, 4, 0><<<grid, held_threads(a.C, 4, 4), 0, s>>>(a);
-        else if (a.C <= 1024) k_norm_held<XT, YT, 1, 8, 128><<<grid, 128, 0, s>>>(a);
+        else if (XT != kMXI8 && !a.codes && a.C <= 8192) {
+            if constexpr (XT != kMXI8)
+                return a.C <= 1024   ? launch_kept<XT, YT, 8, 128>(a, s)
+                       : a.C <= 4096 ? launch_kept<XT, YT, 8, 512>(a, s)
+                       : a.C <= 6144 ? launch_kept<XT, YT, 16, 384>(a, s)
+                                     : launch_kept<XT, YT, 8, 1024>(a, s);
+        } else if (a.C <= 1024) k_norm_held<XT, YT, 1, 8, 128><<<grid, 128, 0, s>>>(a);
         else if (a.C <= 6144) k_norm_held<XT, YT, 1, 16, 384><<<grid, 384, 0, s>>>(a);
         else k_norm_held<XT, YT, 1, 16, 1024><<<grid, 1024, 0, s>>>(a);
         return cudaGetLastError();
