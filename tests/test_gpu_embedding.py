@@ -115,6 +115,24 @@ def test_tokens_beyond_the_table_are_reported():
     e2f.e2f_embedding_backward(cfg, ok, g[:1])
 
 
+@pytest.mark.parametrize("n,V", [(300, 5), (30000, 5), (30000, 256), (300, 3000), (30000, 3000), (30000, 70000)])
+def test_one_token_beyond_the_table_among_many(n, V):
+    """Found wherever it lies, in one tile or many, and gone from the status in the next call."""
+    tok = _tokens(n, V, "uniform").cuda()
+    g = torch.randn(n, 1, 8, device="cuda")
+    cfg = e2f.make_embed_cfg(V, 8)
+    ws = torch.empty(e2f.e2f_embedding_backward_workspace_size(n, cfg), dtype=torch.uint8, device="cuda")
+    bad = tok.clone()
+    bad[2 * n // 3] = V
+    tok[2 * n // 3] = -1
+    want = e2f.e2f_embedding_backward(cfg, tok, g, workspace=ws)
+    with pytest.raises(e2f.E2FError) as e:
+        e2f.e2f_embedding_backward(cfg, bad, g, workspace=ws)
+    assert e.value.code == 1
+    assert torch.equal(e2f.e2f_embedding_backward(cfg, bad, g, workspace=ws, check=False), want)
+    assert torch.equal(e2f.e2f_embedding_backward(cfg, tok, g, workspace=ws), want)
+
+
 @pytest.mark.parametrize("V", [90, 3000])
 def test_streams_capture_and_rows_behind(V):
     n, C = 3000, 64

@@ -137,6 +137,25 @@ def test_long_batches(n, L, C, xt):
         _within(g[name], want, bound, name)
 
 
+@pytest.mark.parametrize("yt", ["f32", "bf16"])
+@pytest.mark.parametrize("xt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,L,C", [(5000, 0, 1001), (900, 0, 259), (1200, 0, 2049), (1500, 0, 5001), (700, 0, 8190),
+                                   (400, 0, 9001), (2000, 2, 100), (2000, 2, 101), (1500, 0, 4096), (400, 1, 300)])
+def test_residual_without_a_checkpoint(n, L, C, xt, yt):
+    """Several rows a block, the stream updated in place or not: the same bits, within the forward's bounds."""
+    x, w, b, r = _x(n, L, C, xt, seed=n + C + 5)
+    cfg = e2f.make_norm_cfg(L, C, xt, yt, EPS)
+    f = e2f.e2f_layer_norm(cfg, x.cuda(), w.cuda(), b.cuda(), residual=r.cuda())
+    h = (x.float() + r).to(x.dtype)
+    assert torch.equal(f["sum"].cpu(), h)
+    _check_forward((xt, yt), f, h, w, b, L)
+    at = x.cuda()
+    g = e2f.e2f_layer_norm(cfg, at, w.cuda(), b.cuda(), residual=r.cuda(), out={"sum": at})
+    assert all(torch.equal(f[k], g[k]) for k in f)
+    p = e2f.e2f_layer_norm(cfg, f["sum"], w.cuda(), None)
+    _check_forward((xt, yt), p, h, w, None, L)
+
+
 @pytest.mark.parametrize("n,L,C", [(9, 4, 128), (20, 0, 1000), (6, 2, 33)])
 def test_gradient_against_differences(n, L, C):
     """The kernel's gradients along a random direction against a central difference of the 64-bit forward (which
