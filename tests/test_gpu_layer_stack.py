@@ -150,3 +150,43 @@ def test_forward_captured_and_replayed():
     now, kept2 = s.forward(check=False)
     # the attention sums in a fixed order: the same bits
     assert torch.equal(held, now) and all(torch.equal(a["codes"], b["codes"]) for a, b in zip(kept, kept2))
+
+
+def test_offsets_beyond_32_bits():
+    """700,000 atoms at L = 4, C = 128: 2.24 G values. The last atoms come out as they do alone."""
+    n, L, C, V = 700_000, 4, 128, 7
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.empty(n, 25, C, dtype=torch.bfloat16, device=dev()).normal_(generator=gen)
+    gy = torch.zeros(n, 25, C, device=dev())
+    gy[-40:].normal_(generator=gen)
+    w, b = torch.randn(L + 1, C, device=dev()), torch.randn(C, device=dev())
+    cfg = e2f.make_norm_cfg(L, C, "bf16", "bf16", EPS)
+    big = e2f.e2f_layer_norm(cfg, x, w, b, checkpoint=True)
+    end = x[-40:].contiguous()
+    small = e2f.e2f_layer_norm(cfg, end, w, b, checkpoint=True)
+    for k in small:
+        assert torch.equal(big[k][-40:], small[k]), k
+    g = e2f.e2f_layer_norm_backward(cfg, x, w, big["mean"], big["rstd"], gy)
+    gs = e2f.e2f_layer_norm_backward(cfg, end, w, small["mean"], small["rstd"], gy[-40:].contiguous())
+    assert torch.equal(g["x"][-40:], gs["x"]) and (g["x"][:-40] == 0).all()
+    # the weight sums differ in their order only: 40 nodes' rows, the rest adds zeros
+    xh = R.norm(end.cpu().double(), torch.ones(L + 1, C, dtype=torch.float64), None, L, EPS)[0]
+    for l, rows in enumerate(R.degrees(L)):
+        mag = (gy[-40:, rows].cpu().double() * xh[:, rows]).abs().sum((0, 1))
+        assert ((g["weight"][l] - gs["weight"][l]).cpu().double().abs() <= 2 * 1024 * R.U * mag).all()
+    del g, big
+    codes, scales = e2f.e2f_checkpoint_store(x)
+    assert torch.equal(codes[-40:], small["codes"]) and torch.equal(scales[-40:], small["scales"])
+    back = e2f.e2f_checkpoint_load(codes, scales, "bf16")
+    assert torch.equal(back[-40:], e2f.e2f_checkpoint_load(small["codes"], small["scales"], "bf16"))
+    del codes, scales, back, x
+    tok = torch.randint(0, V, (n,), dtype=torch.int32, device=dev(), generator=gen)
+    for rows in (V, 1000):  # both ways of sorting
+        ecfg = e2f.make_embed_cfg(rows, C, L, 1.0, "f32", "bf16")
+        grad = e2f.e2f_embedding_backward(ecfg, tok, gy)
+        want, mag = R.embedding_backward(tok[-40:].cpu(), gy[-40:].cpu(), rows, 1.0)
+        assert ((grad.cpu().double() - want).abs() <= 1024 * R.U * mag).all()
+        table = torch.randn(rows, C, device=dev())
+        out = e2f.e2f_embedding(ecfg, tok, table)
+        assert torch.equal(out[-40:], e2f.e2f_embedding(ecfg, tok[-40:].contiguous(), table))
+        del out
