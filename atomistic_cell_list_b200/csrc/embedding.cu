@@ -583,9 +583,11 @@ cudaError_t run_embed_bwd(const e2f_embed_cfg& f, const int32_t* tok, int64_t n,
         idx[k] = reinterpret_cast<int*>(ws + w.o_idx[k]);
     }
     const unsigned tiles = (unsigned)w.sort_tiles;
-    const int64_t values = (int64_t)f.n_tokens * f.C, share = (values / (3 * w.passes) + 4095) / 4096 * 4096;
+    // equal shares for the sort's kernels, in whole 4,096s, both divisions rounded up: together no less than `values`
+    const int64_t values = (int64_t)f.n_tokens * f.C, kernels = 3 * w.passes;
+    const int64_t share = ((values + kernels - 1) / kernels + 4095) / 4096 * 4096;
     int64_t zeroed = 0;
-    auto zeros = [&]() {  // the next share, the rest in the last kernel's
+    auto zeros = [&]() {  // the next share; the last ones may be shorter or empty
         const Zeros z{grad, zeroed, std::min(share, values - zeroed)};
         zeroed += z.n;
         return z;

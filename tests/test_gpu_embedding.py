@@ -166,3 +166,17 @@ def test_streams_capture_and_rows_behind(V):
     assert (big[n:] == 77).all() and (tall[V:] == 77).all() and torch.equal(tall[:V], now[1])
     with pytest.raises(ValueError):
         e2f.e2f_embedding_backward(cfg, tok, g[:, :1])
+
+
+@pytest.mark.parametrize("V,C", [(1229, 20), (6145, 4), (8193, 3), (4337, 17), (69121, 8), (70042, 20)])
+def test_rows_without_tokens_are_zero_to_the_end_of_the_table(V, C):
+    """Tables of which the zeroing kernels' equal shares leave a remainder; the tokens are all below V/2, so that
+    nothing but the zeroing writes the last rows."""
+    n = 300
+    tok = _tokens(n, V // 2, "uniform", seed=V)
+    g = torch.randn(n, 1, C, generator=torch.Generator().manual_seed(3))
+    got = e2f.e2f_embedding_backward(e2f.make_embed_cfg(V, C, 0, 0.7), tok.cuda(), g.cuda(),
+                                     out=torch.full((V, C), 77.0, device="cuda"))
+    want, mag = R.embedding_backward(tok, g, V, 0.7)
+    assert (got[V // 2:] == 0).all()
+    assert ((got.cpu().double() - want).abs() <= (CHAIN + 4) * R.U * mag).all()
