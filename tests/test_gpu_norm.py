@@ -1,5 +1,8 @@
 """e2f_layer_norm and e2f_layer_norm_backward against the plain 64-bit implementation, element by element within
 the rounding bounds of tests/feature_ref.py, on every input and output type, from one row to long odd ones."""
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -306,3 +309,37 @@ def test_refusals():
     with pytest.raises(e2f.E2FError) as e:
         e2f.e2f_layer_norm(cfg, torch.zeros(4 * 4 * 16 + 1, device="cuda")[1:].view(4, 4, 16), w)
     assert e.value.code == 4
+
+
+AROUND_48_KB = """
+import sys
+sys.path[:0] = %r
+import torch, atomistic_cell_list_b200 as e2f, feature_ref as R, test_gpu_norm as T
+n, L, failed = 2, 1, []
+for xt in ("f32", "bf16", "mxi8"):
+    for C in (6128, 6129, 6144):
+        x, w, b, gy = T._x(n, L, C, "f32" if xt == "mxi8" else xt, seed=C)
+        h, dev, scales = x.double(), x.cuda(), None
+        if xt == "mxi8":
+            h, code, byte = R.coded(x)
+            dev, scales = code.cuda(), byte.cuda()
+        _, mean, rstd = (t.float() for t in R.norm(h, w.double(), None, L, T.EPS))
+        try:
+            g = e2f.e2f_layer_norm_backward(e2f.make_norm_cfg(L, C, xt, "f32", T.EPS), dev, w.cuda(), mean.cuda(),
+                                            rstd.cuda(), gy.cuda(), x_scales=scales)
+        except e2f.E2FError as e:
+            failed.append((xt, C, str(e)))
+            continue
+        ref = (h, w.double(), mean.double(), rstd.double(), gy.double(), L)
+        for name, want, bound in zip(("x", "weight", "bias"), R.norm_backward(*ref), R.norm_backward_bound(*ref)):
+            T._within(g[name], want, bound, name)
+assert not failed, failed
+"""
+
+
+def test_weight_gradients_around_48_kb_of_shared_memory():
+    """A row's weight and bias sums (8 C bytes) and the block's own 128 bytes together pass, at 6,129 channels, the
+    shared memory that a launch has without asking. In a process of its own, in this order: a call with more
+    channels raises the limit for all later ones."""
+    r = subprocess.run([sys.executable, "-c", AROUND_48_KB % sys.path], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
