@@ -63,15 +63,20 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
         __syncwarp();
         const uint32_t st = mine_s + s * sl.stage_bytes;
         const float* stat = reinterpret_cast<const float*>(smem + (st - smem_s) + sl.o3) + team * B;
+        const float* mean[NI];  // of lanes beyond the row: zero, for (0 - mean) rstd may be infinite and 0 times it NaN
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            mean[i] = in[i] ? stat + kStatNodes : reinterpret_cast<const float*>(smem + (zeros - smem_s));
         float x[B][R][NI][V], g[B][R][NI][V], r[B], s1[B], s2[B];  // x becomes xh, g becomes u = grad_y weight
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             r[b] = stat[b];
             s1[b] = s2[b] = 0.f;
-            const float mu = l == 0 ? stat[kStatNodes + b] : 0.f;
             const bool ok = b < u.have;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
+                // lanes beyond the row: zero, not (0 - mean) rstd, which may be infinite
+                const float mu = l == 0 ? mean[i][b] : 0.f;
                 const uint32_t p = in[i] ? st + (team0 * C + c[i]) * E : zeros;
                 const uint32_t pg = in[i] ? st + sl.o1 + (team0 * C + c[i]) * 4 : zeros;
                 const int pitch = in[i] ? C : 0;

@@ -343,3 +343,21 @@ def test_weight_gradients_around_48_kb_of_shared_memory():
     channels raises the limit for all later ones."""
     r = subprocess.run([sys.executable, "-c", AROUND_48_KB % sys.path], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("C", [4, 8, 96, 192])
+def test_backward_of_equal_channels_near_the_largest_value(C):
+    """Channels of equal, huge values (a power of two, whose sum and mean are exact): xh is zero and the gradient
+    finite, though mean x rstd, which no value of the row stands for, leaves the fp32 range."""
+    n, top = 5, 2.0 ** 120
+    x = torch.full((n, 1, C), top)
+    _, w, b, gy = _x(n, 0, C, "f32")
+    cfg = e2f.make_norm_cfg(0, C, "f32", "f32", EPS)
+    f = e2f.e2f_layer_norm(cfg, x.cuda(), w.cuda(), b.cuda())
+    mean, rstd = torch.full((n,), top), torch.full((n, 1), EPS, dtype=torch.float64).rsqrt().float()
+    assert torch.equal(f["mean"].cpu(), mean)
+    assert ((f["rstd"].cpu() - rstd).abs() <= 4 * R.U * rstd).all()
+    g = e2f.e2f_layer_norm_backward(cfg, x.cuda(), w.cuda(), mean.cuda(), rstd.cuda(), gy.cuda())
+    ref = (x.double(), w.double(), mean.double(), rstd.double(), gy.double(), 0)
+    for name, want, bound in zip(("x", "weight", "bias"), R.norm_backward(*ref), R.norm_backward_bound(*ref)):
+        _within(g[name], want, bound, name)
