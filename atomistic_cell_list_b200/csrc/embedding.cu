@@ -29,6 +29,7 @@ constexpr int kMaxEmbedC = 16384;
 constexpr int kSortTile = 1024;  // tokens of a sorting block (256 threads, 4 each)
 constexpr int kLocalTokens = 256;  // largest table whose tiles are sorted one by one
 constexpr int kMaxTile = 2048;
+constexpr int64_t kMostTiles = 296;  // two an SM, as long as tiles can grow
 
 struct EmbedWs {
     size_t o_status, o_hist, o_tot, o_key[2], o_idx[2], o_part, bytes;
@@ -46,13 +47,17 @@ EmbedWs embed_layout(int64_t n, const e2f_embed_cfg& c) {
     // up to two tiles per SM, 8 tokens a team at least; what one block sorts fast goes to one block
     const bool local = c.n_tokens <= kLocalTokens;
     w.tile = std::max(64, 8 * (256 / w.TL));
-    while (w.tile < kMaxTile && (n + w.tile - 1) / w.tile > 296) w.tile *= 2;
+    // Where a tile grows there are fewer of them. The workspace has room for the most that n or fewer tokens have,
+    // so that one made for the largest batch serves every smaller one.
+    const auto tiles_of = [n](int tile) { return (n + tile - 1) / tile; };
+    const int64_t room = local && n <= 512 ? 1 : std::max(std::min(tiles_of(w.tile), kMostTiles), tiles_of(kMaxTile));
+    while (w.tile < kMaxTile && tiles_of(w.tile) > kMostTiles) w.tile *= 2;
     if (local && n <= 512) w.tile = std::max(w.tile, 512);
-    w.tiles = (n + w.tile - 1) / w.tile;
+    w.tiles = tiles_of(w.tile);
     w.o_status = take(256);  // first: e2f_attention_status reads it
     if (local) {
-        w.o_hist = take((size_t)w.tiles * (c.n_tokens + 1));  // which tokens a tile has, whether one is beyond the table
-        w.o_part = take(w.tiles > 1 ? 4 * (size_t)w.tiles * c.n_tokens * c.C : 0);
+        w.o_hist = take((size_t)room * (c.n_tokens + 1));  // which tokens a tile has, whether one is beyond the table
+        w.o_part = take(room > 1 ? 4 * (size_t)room * c.n_tokens * c.C : 0);
     } else {
         w.passes = 1;
         while (w.passes < 4 && ((int64_t)c.n_tokens >> (8 * w.passes))) ++w.passes;
@@ -63,7 +68,7 @@ EmbedWs embed_layout(int64_t n, const e2f_embed_cfg& c) {
             w.o_key[k] = take(4 * (size_t)n);
             w.o_idx[k] = take(4 * (size_t)n);
         }
-        w.o_part = take(8 * (size_t)w.tiles * c.C);
+        w.o_part = take(8 * (size_t)room * c.C);
     }
     w.bytes = o;
     return w;

@@ -651,7 +651,9 @@ e2f_status e2f_checkpoint_load(const int8_t* codes, const uint8_t* scales,
  *              not occur become zero).
  *   workspace  forward: NULL (tokens >= n_tokens go unreported) or >= 256
  *              bytes; backward: >= e2f_embedding_backward_workspace_size
- *              bytes. 256-byte aligned, not shared by calls in flight.
+ *              bytes, which do not fall as n_atoms grows: a workspace made for
+ *              the largest batch serves every smaller one. 256-byte aligned,
+ *              not shared by calls in flight.
  * table, out, grad_out, grad_table 16-byte aligned. The backward sorts the
  * tokens and sums each token's rows in a fixed order: results repeat bit for
  * bit. Asynchronous, may be captured into a graph.

@@ -180,3 +180,19 @@ def test_rows_without_tokens_are_zero_to_the_end_of_the_table(V, C):
     want, mag = R.embedding_backward(tok, g, V, 0.7)
     assert (got[V // 2:] == 0).all()
     assert ((got.cpu().double() - want).abs() <= (CHAIN + 4) * R.U * mag).all()
+
+
+@pytest.mark.parametrize("V", [100, 300])
+def test_a_small_batch_in_the_workspace_of_a_large_one(V):
+    """The status word of every call lies in the caller's workspace, whichever batch it was made for."""
+    C, most = 128, 19000
+    cfg = e2f.make_embed_cfg(V, C)
+    ws = torch.empty(e2f.e2f_embedding_backward_workspace_size(most, cfg), dtype=torch.uint8, device="cuda")
+    for n in (18945, 18944, 513, 512, 1):
+        tok, g = _tokens(n, V, "uniform", seed=n, pad=0.0), torch.randn(n, 1, C)
+        tok[n // 2] = V
+        ws[:4] = 77
+        got = e2f.e2f_embedding_backward(cfg, tok.cuda(), g.cuda(), workspace=ws, check=False)
+        assert e2f.lib().e2f_attention_status(ws.data_ptr(), ws.numel(), None) == 1
+        want, mag = R.embedding_backward(tok, g, V, 1.0)
+        assert ((got.cpu().double() - want).abs() <= (CHAIN + 4) * R.U * mag).all()

@@ -140,3 +140,14 @@ def test_binding_refuses_tensors_of_another_kind():
         e2f.e2f_embedding(e2f.make_embed_cfg(9, 16), torch.zeros(3, dtype=torch.int64), torch.zeros(9, 16))
     with pytest.raises(KeyError):
         e2f.make_norm_cfg(1, 16, "f16")
+
+
+@pytest.mark.parametrize("V,C", [(100, 128), (256, 1024), (256, 16384), (5, 16383), (9, 1), (2, 33), (300, 128),
+                                 (70000, 1024), (257, 16384)])
+def test_workspaces_of_the_table_gradient_do_not_shrink_with_more_atoms(V, C):
+    """One workspace, made for the largest batch, serves every smaller one."""
+    c = e2f.make_embed_cfg(V, C)
+    steps = [1, 63, 64, 65, 511, 512, 513, 18943, 18944, 18945, 19000, 30000, 37888, 37889, 606207, 606208, 606209]
+    steps += [t * b + d for t in (64, 128, 256, 512, 1024, 2048) for b in (2, 37, 74, 148, 296) for d in (-1, 0, 1)]
+    sizes = [e2f.e2f_embedding_backward_workspace_size(n, c) for n in sorted(steps)]
+    assert sizes == sorted(sizes)
