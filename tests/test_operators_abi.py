@@ -151,3 +151,13 @@ def test_workspaces_of_the_table_gradient_do_not_shrink_with_more_atoms(V, C):
     steps += [t * b + d for t in (64, 128, 256, 512, 1024, 2048) for b in (2, 37, 74, 148, 296) for d in (-1, 0, 1)]
     sizes = [e2f.e2f_embedding_backward_workspace_size(n, c) for n in sorted(steps)]
     assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("V,C", [(256, 128), (256, 1024), (256, 8192), (256, 16384), (100, 8191), (2, 16384)])
+@pytest.mark.parametrize("n", [600, 19000, 100000, 600000])
+def test_workspace_of_the_table_gradient_is_no_larger_than_what_it_sums(V, C, n):
+    """The tiles' partial sums take no more than 16 MB or the degree-0 rows of grad_out that they are made of, nor
+    more than 160 MB or a share V / 2048 of those rows (beside them at most 64 bytes an atom: flags and alignment)."""
+    need = e2f.e2f_embedding_backward_workspace_size(n, e2f.make_embed_cfg(V, C))
+    rows = 4 * (n + 2048) * C
+    assert need <= min(max(2 ** 24, rows), max(160e6, rows * V / 2048)) + 64 * n + 4096
