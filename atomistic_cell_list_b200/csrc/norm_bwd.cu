@@ -68,6 +68,7 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
         for (int i = 0; i < NI; ++i)
             mean[i] = in[i] ? stat + kStatNodes : reinterpret_cast<const float*>(smem + (zeros - smem_s));
         float x[B][R][NI][V], g[B][R][NI][V], r[B], s1[B], s2[B];  // x becomes xh, g becomes u = grad_y weight
+        float uw[NI][V] = {}, ub[NI][V] = {};  // the unit's part of dw and db, so that the chains of additions stay short
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             r[b] = stat[b];
@@ -92,10 +93,10 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                     const float gv[V] = {e.a.x, e.a.y, e.a.z, e.a.w};
                     for (int k = 0; k < V; ++k) {
                         const float xh = (l == 0 ? xv[k] - mu : xv[k]) * r[b], uk = gv[k] * w[i][k];
-                        if (ok) dw[i][k] += gv[k] * xh;
+                        if (ok) uw[i][k] += gv[k] * xh;
                         s2[b] += uk * xh;
                         if constexpr (l == 0) {
-                            if (ok) db[i][k] += gv[k];
+                            if (ok) ub[i][k] += gv[k];
                             s1[b] += uk;
                         }
                         xv[k] = xh;
@@ -104,6 +105,12 @@ __device__ __forceinline__ void norm_bwd_degree(const NormBwdArgs& a, int TL, co
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            for (int k = 0; k < V; ++k) {
+                dw[i][k] += uw[i][k];
+                if constexpr (l == 0) db[i][k] += ub[i][k];
+            }
         if constexpr (XT == kMXI8)
             if (k + step < units) U(k + step, a.n, K, TL).scales(a.xs, a.nb, K, TL, c, scale);
         if constexpr (l == 0) team_sum(s1, TL);

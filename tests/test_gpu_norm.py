@@ -361,3 +361,24 @@ def test_backward_of_equal_channels_near_the_largest_value(C):
     ref = (x.double(), w.double(), mean.double(), rstd.double(), gy.double(), 0)
     for name, want, bound in zip(("x", "weight", "bias"), R.norm_backward(*ref), R.norm_backward_bound(*ref)):
         _within(g[name], want, bound, name)
+
+
+@pytest.mark.parametrize("n,L,xt", [(2000000, 0, "f32"), (100000, 4, "bf16"), (30000, 2, "f32")])
+def test_weight_gradients_of_many_rows(n, L, xt):
+    """Equal terms, whose roundings all fall to one side. The chain of additions behind one weight of degree l: the
+    rows of a warp's unit (9, 3, 1, .. nodes), the units of a warp (296 blocks of 4 warps, shared among the degrees by
+    their rows and half a row more each), the block's warps, the blocks of a join's warp and its 5 levels."""
+    C, K, v = 128, (L + 1) ** 2, 1 + 2.0 ** -14 - 2.0 ** -23
+    cfg = e2f.make_norm_cfg(L, C, xt, "f32", EPS)
+    x = torch.ones(n, K, C, device="cuda", dtype=R.DT[xt])
+    w, g = torch.ones(L + 1, C, device="cuda"), torch.full((n, K, C), v, device="cuda")
+    got = e2f.e2f_layer_norm_backward(cfg, x, w, torch.zeros(n, device="cuda"), torch.ones(n, L + 1, device="cuda"), g,
+                                      out={"x": g})
+    for l in range(L + 1):
+        rows, nodes = 2 * l + 1, (9, 3, 1, 1, 1)[l]
+        blocks = int(296 * (rows + 0.5) / (K + 0.5 * (L + 1)))
+        chain = nodes * rows + -(-n // (nodes * blocks * 4)) + 4 + -(-blocks // 32) + 5
+        want = torch.full((C,), n * rows * v, dtype=torch.float64)
+        _within(got["weight"][l], want, chain * R.U * want, f"weight {l}")
+        if l == 0:
+            _within(got["bias"], want, chain * R.U * want, "bias")
