@@ -196,3 +196,20 @@ def test_a_small_batch_in_the_workspace_of_a_large_one(V):
         assert e2f.lib().e2f_attention_status(ws.data_ptr(), ws.numel(), None) == 1
         want, mag = R.embedding_backward(tok, g, V, 1.0)
         assert ((got.cpu().double() - want).abs() <= (CHAIN + 4) * R.U * mag).all()
+
+
+# the same for batches whose tiles grow to 2,048 tokens: tile/teams rows of a team, the first and last runs of the
+# tile's teams, the tiles of a join's warp, 16 warps. C = 128: 256 + 2 x 8 + 19 + 16; C = 16: 32 + 2 x 64 + 19 + 16
+LONG_CHAIN = 310
+
+
+@pytest.mark.parametrize("kind", ["uniform", "two", "skewed"])
+@pytest.mark.parametrize("n,V,C", [(100000, 100, 128), (300000, 300, 128), (620000, 7, 128), (620000, 5000, 128),
+                                   (610000, 3, 16), (30000, 256, 1024)])
+def test_gradient_of_long_tiles(n, V, C, kind):
+    tok = _tokens(n, V, kind, seed=n)
+    g = torch.randn(n, 1, C, generator=torch.Generator().manual_seed(4))
+    cfg = e2f.make_embed_cfg(V, C, 0, 0.7)
+    got = e2f.e2f_embedding_backward(cfg, tok.cuda(), g.cuda(), out=torch.full((V, C), 77.0, device="cuda"))
+    want, mag = R.embedding_backward(tok, g, V, 0.7)
+    assert ((got.cpu().double() - want).abs() <= (LONG_CHAIN + 4) * R.U * mag).all()
