@@ -246,7 +246,7 @@ __global__ void k_norm_bwd_rows(NormBwdArgs a) {
 // each value is read once, and a row's loads are issued before the sums of the row
 // before it. 8,192 rows of 4,096 fp32 values with a skip gradient: 537 MB in 101 us
 // (5.3 TB/s; 113 us without the early loads). 20,000 rows of 1,001, value by value:
-// 54 us; 4,096 rows of 5,001 with bf16 x: 85 us, bound by instructions.
+// 54 us; 4,096 rows of 5,001 with bf16 x: 79 us, bound by instructions.
 // part: [block][C], then [block][C] for the bias.
 template <int XT, int V, int NV, int TT>
 __global__ void __launch_bounds__(TT ? TT : 1024) k_norm_bwd_held(NormBwdArgs a) {
@@ -383,10 +383,12 @@ int bwd_held(int L, int C) {
     return C <= 1024 ? 128 : C <= 6144 ? 512 : 0;
 }
 
-// blocks of k_norm_bwd_held (at most 1,024 threads and 5 blocks an SM, what fits at
-// once by registers: a second wave costs more than it hides), or blocks per row of features of k_norm_bwd_rows
+// blocks of k_norm_bwd_held (what fits at once by registers: 1,024 threads of 64, at most 5 blocks, and one block of
+// 512 threads of 128, value by value; a second wave costs more than it hides: 4,096 rows of 5,001 bf16 values 79 us
+// in 148 blocks, 85 us in 296), or blocks per row of features of k_norm_bwd_rows
 int rows_blocks(int64_t n, int L, int C) {
-    const int t = bwd_held(L, C), most = t ? kSMs * std::max(1, std::min(5, 1024 / t)) : kNormBlocks / ((L + 1) * (L + 1));
+    const int t = bwd_held(L, C), threads = t == 512 && C % 4 ? 512 : 1024;
+    const int most = t ? kSMs * std::max(1, std::min(5, threads / t)) : kNormBlocks / ((L + 1) * (L + 1));
     return (int)std::max<int64_t>(1, std::min<int64_t>(n, most));
 }
 
