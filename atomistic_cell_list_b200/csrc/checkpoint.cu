@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(256) k_ck_load_flat(const int8_t* codes, const
     }
 }
 
-// any C: 32/V lanes per block of channels
+// any C: 32/V lanes per block of channels, found by divisions. 30,000 atoms, L = 4, bf16,
+// store and load together: C = 100 (228 MB a way) 161 us, C = 101, value by value, 556 us.
 template <int T, int V>
 __global__ void __launch_bounds__(256) k_ck_store(const void* x, int64_t rows, int C, int nb, int8_t* codes,
                                                   uint8_t* scales) {

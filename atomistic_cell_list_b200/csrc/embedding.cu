@@ -108,7 +108,7 @@ constexpr int kWide = T == kBF16 ? 8 : 4;
 // One group of `lanes` lanes (a power of two) per node: its first C values from
 // the table, zeros behind them. V values a store; the write of the output bounds it:
 // 100,000 atoms, L = 4, C = 128 in bf16, 640 MB in 94 us (6.8 TB/s; with a division
-// per 8 bytes it was 222 us).
+// per 8 bytes it was 222 us); C = 132, which no 16 bytes divide, value by value: 660 MB in 123 us.
 template <int TT, int YT, int V>
 __global__ void __launch_bounds__(256) k_embed(const int32_t* tok, int64_t n, const void* table, int n_tokens, int K,
                                                int C, float scale, int lanes, void* out, int* status) {
@@ -411,8 +411,8 @@ __global__ void __launch_bounds__(256) k_run_sum(RunArgs a) {
         for (int p = p0; p < p1; p += U) {
             uint32_t key[U];
             float v[U][V];
-            // every load is made, so that all are in flight: padding and what lies behind the part read the
-            // batch's first row, lanes beyond the columns the first column, and count as zero
+            // every load is made, so that all are in flight: what lies behind the part reads the batch's first row,
+            // lanes beyond the columns the first column, padding its own row, and none of it counts
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const int at = p + j < p1 ? p + j : p;

@@ -7,7 +7,8 @@
 // and with xh = d r, u = grad_y weight:
 //   grad_x = r (u - xh mean(u xh)  [- mean u for l = 0]) (+ grad_skip)
 //   grad_weight[l,c] = sum_{n,m} grad_y xh,   grad_bias[c] = sum_n grad_y[n,0,c]
-// All sums are fp32. A few operations per value: memory bound.
+// All sums are fp32, those of the weight's gradient in chains of a unit's rows, then of
+// units. A few operations per value: memory bound.
 //
 // C a multiple of 4 up to 256 (the attention takes multiples of 16): a team of TL lanes (a
 // power of two, TL >= C/4 up to 32) owns whole rows, lane t the channels
@@ -21,8 +22,9 @@
 // one another, and the bytes in flight (about 100 KB an SM) do not depend on
 // registers or occupancy. Lanes beyond the row read zeros.
 // Other C up to 256: one warp per unit, values one by one (norm_scalar.cu).
-// L = 0 with more channels: one block per row, the row in registers. The rest: one
-// block per (node, degree), which reads its group once per pass.
+// L = 0 with more channels: a block per row, or persistent blocks that go from row to
+// row, the row in registers. The rest: one block per (node, degree), which reads its
+// group once per pass.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -527,7 +527,8 @@ e2f_status e2f_sixj_attention(const e2f_sixj_cfg* cfg, const float* pos, int64_t
  * A degree's rows share one factor and the mean touches l = 0 only, so the
  * norm commutes with rotations. A NaN or an infinity reaches the outputs of
  * its own group and nothing else. Sums are fp32; groups whose d^2 leaves the
- * fp32 range (|d| above about 1e19) give rstd = 0.
+ * fp32 range (|d| above about 1e19) give rstd = 0, and NaN in y where the sum
+ * of the channels itself leaves it.
  *
  *   cfg        host; L (0..4), C (1..16384), eps > 0, x_dtype (E2F_F32,
  *              E2F_BF16 or E2F_MXI8: x is a checkpoint), y_dtype (E2F_F32 or
